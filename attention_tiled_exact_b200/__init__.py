@@ -15,6 +15,13 @@ step of the computation runs in its CUDA kernels):
 * :func:`decode_paged_noalloc` -- decode for callers that cannot allocate;
 * :class:`PersistentDecode` -- a resident decode kernel driven step by step;
 * :class:`DecodeGraphPool` -- CUDA graphs of the decode step per static shape;
+* :func:`plan_paged_step` -- block tables, positions and slots of a serving
+  step, built on the device;
+* :func:`rotary` -- rotary positions on queries and keys, and their gradient;
+* :func:`append_paged` / :func:`gather_paged` -- new tokens into the pages of a
+  bf16 or block-scaled 8-bit cache (with rotary positions), and back;
+* :func:`decode_paged_block_scaled` / :func:`prefill_paged_block_scaled` --
+  attention over the block-scaled 8-bit cache;
 * :func:`splitkv_lse_combine` -- log-sum-exp merge of split partials;
 * :func:`sync_error_flags` / :func:`status_from_flags` -- the device error
   word as a status;
@@ -27,6 +34,8 @@ fallback.
 """
 _API = ("prefill", "prefill_paged", "prefill_from_host", "prefill_backward", "decode_paged", "decode_workspace_bytes",
         "decode_paged_shared_prefix", "decode_shared_prefix_workspace_bytes", "decode_paged_noalloc",
+        "plan_paged_step", "rotary", "append_paged", "gather_paged", "decode_paged_block_scaled",
+        "prefill_paged_block_scaled",
         "splitkv_lse_combine", "sync_error_flags", "status_from_flags", "set_wait_limit", "selftest_exp2",
         "debug_bounds_enabled", "debug_plant_bounds",
         "PersistentDecode", "DecodeGraphPool",

@@ -40,6 +40,7 @@ ATTN_FAULT_BAD_BLOCK = 0x2
 ATTN_FAULT_BAD_LENGTH = 0x4
 ATTN_FAULT_PREFIX_MISMATCH = 0x8
 ATTN_FAULT_BOUNDS = 0x10
+ATTN_FAULT_NO_BLOCK = 0x20
 
 # Bounds-check sites of the debug build (attn_bounds_site_t).
 BOUNDS_SITES = {
@@ -110,6 +111,53 @@ class DecodeParams(ctypes.Structure):
     ]
 
 
+class RotaryParams(ctypes.Structure):
+    """Mirror of ``attn_rotary_params``."""
+
+    _fields_ = [
+        ("q", _vp), ("k", _vp), ("q_out", _vp), ("k_out", _vp), ("positions", _vp), ("inv_freq", _vp),
+        ("batch", _i32), ("num_q_heads", _i32), ("num_k_heads", _i32), ("seqlen", _i32), ("head_dim", _i32),
+        ("rotary_dim", _i32), ("interleaved", _i32), ("inverse", _i32), ("magnitude", ctypes.c_float),
+        ("in_dtype", _i32), ("out_dtype", _i32),
+    ] + [(f"{t}_{d}_stride", _i64) for t in ("q", "k", "qo", "ko") for d in ("batch", "head", "row")]
+
+
+class PlanParams(ctypes.Structure):
+    """Mirror of ``attn_plan_params``."""
+
+    _fields_ = [
+        ("seq_lens", _vp), ("new_lens", _vp), ("block_table", _vp), ("free_blocks", _vp), ("num_used", _vp),
+        ("seq_lens_out", _vp), ("cu_seqlens_q", _vp), ("positions", _vp), ("slot_map", _vp), ("num_used_out", _vp),
+        ("error_flags", _vp), ("batch", _i32), ("max_blocks_per_seq", _i32), ("num_blocks", _i32),
+        ("num_free", _i32), ("total_q", _i32), ("block_size", _i32),
+    ]
+
+
+class AppendParams(ctypes.Structure):
+    """Mirror of ``attn_append_params``."""
+
+    _fields_ = [
+        ("q", _vp), ("q_out", _vp), ("k", _vp), ("v", _vp), ("k_cache", _vp), ("v_cache", _vp),
+        ("k_scales", _vp), ("v_scales", _vp), ("slot_map", _vp), ("positions", _vp), ("inv_freq", _vp),
+        ("error_flags", _vp), ("total", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32),
+        ("num_blocks", _i32), ("block_size", _i32), ("rotary_dim", _i32), ("interleaved", _i32),
+        ("magnitude", ctypes.c_float), ("kv_dtype", _i32),
+        ("q_row_stride", _i64), ("q_head_stride", _i64), ("qo_row_stride", _i64), ("qo_head_stride", _i64),
+        ("k_row_stride", _i64), ("k_head_stride", _i64), ("v_row_stride", _i64), ("v_head_stride", _i64),
+    ]
+
+
+class GatherParams(ctypes.Structure):
+    """Mirror of ``attn_gather_params``."""
+
+    _fields_ = [
+        ("k_cache", _vp), ("v_cache", _vp), ("k_scales", _vp), ("v_scales", _vp), ("block_table", _vp),
+        ("seq_lens", _vp), ("k_out", _vp), ("v_out", _vp), ("error_flags", _vp),
+        ("batch", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("width", _i32),
+        ("num_blocks", _i32), ("block_size", _i32), ("max_blocks_per_seq", _i32), ("kv_dtype", _i32),
+    ]
+
+
 class PersistentCmd(ctypes.Structure):
     """Mirror of ``attn_persistent_cmd`` (host memory shared with the persistent kernel)."""
 
@@ -140,6 +188,15 @@ def _load():
     lib.splitkv_lse_combine.argtypes = [_vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
                                         ctypes.c_int, _vp, _vp]
     lib.splitkv_lse_combine.restype = ctypes.c_int
+    for name, params in (("attn_rotary", RotaryParams), ("attn_plan_paged_step", PlanParams),
+                         ("attn_append_paged", AppendParams), ("attn_gather_paged", GatherParams)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp]
+        getattr(lib, name).restype = ctypes.c_int
+    for name, params in (("attn_decode_paged_block_scaled", DecodeParams),
+                         ("attn_prefill_paged_block_scaled", PrefillParams)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp, _vp, _vp, ctypes.c_size_t,
+                                       ctypes.POINTER(ctypes.c_size_t), _vp]
+        getattr(lib, name).restype = ctypes.c_int
     lib.attn_status_string.argtypes = [ctypes.c_int]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_version.argtypes = []
@@ -613,6 +670,309 @@ def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, out, lse=No
     p = _decode_params(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, num_splits, out, lse,
                        error_flags, k_scale, v_scale)
     _check(LIB.attn_decode_paged_noalloc(ctypes.byref(p), _stream(q.device)), "attn_decode_paged_noalloc")
+    return out, lse
+
+
+# ----------------------------------------------------------------------------
+# a serving step over a paged cache: plan, rotary positions, append, gather, and
+# attention over the block-scaled 8-bit cache
+# ----------------------------------------------------------------------------
+
+
+def _same_device(*tensors):
+    """The one CUDA device of the tensors that are given."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        _need(t.is_cuda and (dev is None or t.device == dev), "CUDA tensors of one device")
+        dev = t.device
+    return dev
+
+
+def _call(fn, where, device, *args):
+    """fn(*args, stream) on the device's current stream, with that device current."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(device)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(device)), where)
+
+
+def _call_with_workspace(fn, where, device, p, k_scales, v_scales, workspace):
+    """Query the workspace size, take the caller's or a new one, and launch."""
+    with torch.cuda.device(device):
+        ref, need = ctypes.byref(p), ctypes.c_size_t(0)
+        _check(fn(ref, _ptr(k_scales), _ptr(v_scales), None, 0, ctypes.byref(need), None), where + "(size)")
+        if workspace is None and need.value > 0:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+        ws_ptr = _ptr(workspace) if workspace is not None else ctypes.c_void_p(0)
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check(fn(ref, _ptr(k_scales), _ptr(v_scales), ws_ptr, ws_bytes, None, _stream(device)), where)
+
+
+def _i32_vec(t, n, what):
+    _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n, f"int32 {what} [{n}]")
+
+
+def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, total_q: int, num_blocks: int,
+                    seq_lens_out=None, cu_seqlens_q=None, positions=None, slot_map=None, num_used_out=None,
+                    error_flags=None):
+    """Block tables, positions and slots of one step over a paged cache, built on the device.
+
+    seq_lens / new_lens (int32 [B]): cached and new tokens of each sequence.
+    block_table (int32 [B, max_blocks]) lists each sequence's blocks; the
+    further blocks a sequence needs are taken from free_blocks (int32) at
+    num_used (int32 [1]) and entered. total_q (host) is the number of rows of
+    the packed step, at least the sum of new_lens; rows behind that sum get
+    position and slot -1, which :func:`rotary` and :func:`append_paged` skip.
+    num_blocks is the pool's size. seq_lens_out may be seq_lens and
+    num_used_out num_used: the state then advances in place.
+    Returns ``(seq_lens_out [B], cu_seqlens_q [B + 1], positions [total_q],
+    slot_map [total_q], num_used_out [1])``.
+    """
+    dev = _same_device(seq_lens, new_lens, block_table, free_blocks, num_used, seq_lens_out, cu_seqlens_q, positions,
+                       slot_map, num_used_out, error_flags)
+    B, total_q = seq_lens.numel(), int(total_q)
+    _need(total_q >= 0, "total_q >= 0")
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.dtype == torch.int32 and
+          block_table.is_contiguous(), "int32 block table [B, max_blocks]")
+    _need(free_blocks.dtype == torch.int32 and free_blocks.is_contiguous(), "int32 free_blocks")
+
+    def out(t, n):
+        return torch.empty(n, dtype=torch.int32, device=dev) if t is None else t
+    seq_lens_out, cu_seqlens_q, num_used_out = out(seq_lens_out, B), out(cu_seqlens_q, B + 1), out(num_used_out, 1)
+    positions, slot_map = out(positions, total_q), out(slot_map, total_q)
+    for t, n, what in ((seq_lens, B, "seq_lens"), (new_lens, B, "new_lens"), (num_used, 1, "num_used"),
+                       (seq_lens_out, B, "seq_lens_out"), (cu_seqlens_q, B + 1, "cu_seqlens_q"),
+                       (num_used_out, 1, "num_used_out"), (positions, total_q, "positions"),
+                       (slot_map, total_q, "slot_map")):
+        _i32_vec(t, n, what)
+    p = PlanParams(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
+                   num_used.data_ptr(), seq_lens_out.data_ptr(), cu_seqlens_q.data_ptr(), positions.data_ptr(),
+                   slot_map.data_ptr(), num_used_out.data_ptr(),
+                   None if error_flags is None else error_flags.data_ptr(), B, block_table.shape[1], int(num_blocks),
+                   free_blocks.numel(), total_q, 16)
+    _call(LIB.attn_plan_paged_step, "attn_plan_paged_step", dev, ctypes.byref(p))
+    return seq_lens_out, cu_seqlens_q, positions, slot_map, num_used_out
+
+
+def _in_code(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return ATTN_DTYPE_BF16
+    _need(dtype == torch.float32, "bfloat16 or float32 rows")
+    return ATTN_DTYPE_F32
+
+
+def _turn_checks(inv_freq):
+    _need(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
+          "float64 inv_freq [rotary_dim / 2]")
+
+
+def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: bool = False, magnitude: float = 1.0,
+           q_out=None, k_out=None, out_dtype=None):
+    """Rotary positions on queries and keys (k may be None), one launch.
+
+    q [B,Hq,S,D] and k [B,Hk,S,D], or packed [T,Hq,D] and [T,Hk,D]; bf16 or
+    fp32. inv_freq (float64 CUDA, [rotary_dim / 2]) holds the radians per
+    position of each pair: a scaling for long contexts is a choice of inv_freq
+    and of ``magnitude``, the factor on the turned elements. positions (int32,
+    [B,S] or [T]; None: 0, 1, ... in each sequence); rows of negative position
+    are not written. The pairs are (i, i + rotary_dim / 2), or (2 i, 2 i + 1)
+    if ``interleaved``; elements from rotary_dim on are copied. ``inverse``
+    turns back: of dQ, dK it gives the gradients of the unrotated q, k.
+    q_out / k_out may be q / k. Returns ``(q_out, k_out)``.
+    """
+    packed = q.dim() == 3
+    _need(packed or q.dim() == 4, "q must be [B, Hq, S, D] or packed [T, Hq, D]")
+    dev = _same_device(q, k, inv_freq, positions, q_out, k_out)
+    _turn_checks(inv_freq)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=out_dtype or k.dtype, device=dev)
+    if packed:
+        B, (S, Hq, D) = 1, q.shape
+    else:
+        B, Hq, S, D = q.shape
+    views = []
+    for x, y in ((q, q_out), (k, k_out)):
+        if x is None:
+            views.append((0, 0, 0, 0, 0, 0))
+            continue
+        _need(x.dim() == q.dim() and x.shape[-1] == D and y.shape == x.shape and
+              ((x.shape[0] == S) if packed else (x.shape[0] == B and x.shape[2] == S)), "shapes of q, k and outputs")
+        _need(x.stride(-1) == 1 and y.stride(-1) == 1, "last dim contiguous")
+        xs, ys = x.stride(), y.stride()
+        views.append((0, xs[1], xs[0], 0, ys[1], ys[0]) if packed else (*xs[:3], *ys[:3]))
+    if k is not None:
+        _need(k.dtype == q.dtype and k_out.dtype == q_out.dtype, "one dtype for q and k")
+    if positions is not None:
+        _i32_vec(positions, B * S, "positions")
+    Hk = 0 if k is None else k.shape[1]
+    (qb, qh, qr, ob, oh, orow), (kb, kh, kr, pb, ph, pr) = views
+    p = RotaryParams(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                     None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
+                     inv_freq.data_ptr(), B, Hq, Hk, S, D, 2 * inv_freq.numel(), int(bool(interleaved)),
+                     int(bool(inverse)), float(magnitude), _in_code(q.dtype), _in_code(q_out.dtype),
+                     qb, qh, qr, kb, kh, kr, ob, oh, orow, pb, ph, pr)
+    _call(LIB.attn_rotary, "attn_rotary", dev, ctypes.byref(p))
+    return q_out, k_out
+
+
+def _pool_checks(k_cache, v_cache, k_scales, v_scales):
+    """Shape and dtype checks of a paged cache; returns its dtype code."""
+    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.shape[2] == 16,
+          "caches [num_blocks, Hkv, 16, D]")
+    _need(k_cache.is_contiguous() and v_cache.is_contiguous() and k_cache.dtype == v_cache.dtype, "contiguous caches")
+    if k_cache.dtype == torch.bfloat16:
+        return ATTN_DTYPE_BF16
+    _need(_is_fp8(k_cache), "bf16 or E4M3 caches")
+    for t in (k_scales, v_scales):
+        _need(t is not None and t.dtype == torch.uint8 and t.is_contiguous() and
+              tuple(t.shape) == tuple(k_cache.shape[:2]), "uint8 scales [num_blocks, Hkv]")
+    return ATTN_DTYPE_FP8_E4M3
+
+
+def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None, q=None, inv_freq=None, positions=None,
+                 interleaved: bool = False, magnitude: float = 1.0, q_out=None, error_flags=None):
+    """Write new tokens into a paged cache, with rotary positions if inv_freq is given.
+
+    k, v [T,Hkv,D] bf16 (any row and head strides); slot_map (int32 [T]: block
+    * 16 + offset, negative: no token). The caches [num_blocks,Hkv,16,D] are
+    bf16, or E4M3 codes (uint8 / float8_e4m3fn) with k_scales / v_scales uint8
+    [num_blocks,Hkv], exponent bytes of a power-of-two scale for each block and
+    head: the scale follows the block's tokens, and a run of new tokens replaces
+    its block from its first slot on (consecutive rows, one run per block and
+    call). inv_freq, positions (int32 [T]), interleaved and magnitude are those
+    of :func:`rotary`; the keys are turned, and so are the queries q [T,Hq,D].
+    Returns the turned queries (q_out, which may be q), or None without q.
+    """
+    dev = _same_device(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, q, inv_freq, positions, q_out, error_flags)
+    code = _pool_checks(k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, _, D = k_cache.shape
+    _need(k.dim() == 3 and v.shape == k.shape and tuple(k.shape[1:]) == (Hkv, D), "k, v [T, Hkv, D]")
+    T = k.shape[0]
+    _need(k.dtype == v.dtype == torch.bfloat16 and k.stride(2) == 1 and v.stride(2) == 1,
+          "bf16 k, v, last dim contiguous")
+    _i32_vec(slot_map, T, "slot_map")
+    p = AppendParams()
+    if q is not None:
+        _need(q.dim() == 3 and q.shape[0] == T and q.shape[2] == D and q.dtype == torch.bfloat16 and q.stride(2) == 1,
+              "bf16 q [T, Hq, D], last dim contiguous")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.stride(2) == 1, "q_out like q")
+        p.q, p.q_out, p.num_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+        p.q_row_stride, p.q_head_stride, _ = q.stride()
+        p.qo_row_stride, p.qo_head_stride, _ = q_out.stride()
+    if inv_freq is not None:
+        _turn_checks(inv_freq)
+        _need(positions is not None, "positions of the rows to turn")
+        _i32_vec(positions, T, "positions")
+        p.inv_freq, p.positions, p.rotary_dim = inv_freq.data_ptr(), positions.data_ptr(), 2 * inv_freq.numel()
+        p.interleaved, p.magnitude = int(bool(interleaved)), float(magnitude)
+    p.k, p.v, p.k_cache, p.v_cache = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    if code == ATTN_DTYPE_FP8_E4M3:
+        p.k_scales, p.v_scales = k_scales.data_ptr(), v_scales.data_ptr()
+    p.slot_map, p.error_flags = slot_map.data_ptr(), None if error_flags is None else error_flags.data_ptr()
+    p.total, p.num_kv_heads, p.head_dim, p.num_blocks, p.block_size, p.kv_dtype = T, Hkv, D, NB, 16, code
+    p.k_row_stride, p.k_head_stride, _ = k.stride()
+    p.v_row_stride, p.v_head_stride, _ = v.stride()
+    _call(LIB.attn_append_paged, "attn_append_paged", dev, ctypes.byref(p))
+    return q_out if q is not None else None
+
+
+def gather_paged(k_cache, v_cache, block_table, seq_lens, width: int, k_scales=None, v_scales=None, k_out=None,
+                 v_out=None, error_flags=None):
+    """The cached values of each sequence as dense bf16 ``(K, V)`` [B,Hkv,width,D].
+
+    The caches and scales are those of :func:`append_paged`; rows from
+    seq_lens[b] on are 0.
+    """
+    dev = _same_device(k_cache, v_cache, block_table, seq_lens, k_scales, v_scales, k_out, v_out, error_flags)
+    code = _pool_checks(k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, _, D = k_cache.shape
+    B, width = block_table.shape[0], int(width)
+    _need(block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2,
+          "int32 block table [B, max_blocks]")
+    _i32_vec(seq_lens, B, "seq_lens")
+    _need(width >= 0, "width >= 0")
+    if k_out is None:
+        k_out = torch.empty((B, Hkv, width, D), dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty((B, Hkv, width, D), dtype=torch.bfloat16, device=dev)
+    for t in (k_out, v_out):
+        _need(tuple(t.shape) == (B, Hkv, width, D) and t.dtype == torch.bfloat16 and t.is_contiguous(),
+              "contiguous bf16 outputs [B, Hkv, width, D]")
+    scales = (k_scales.data_ptr(), v_scales.data_ptr()) if code == ATTN_DTYPE_FP8_E4M3 else (None, None)
+    p = GatherParams(k_cache.data_ptr(), v_cache.data_ptr(), *scales, block_table.data_ptr(), seq_lens.data_ptr(),
+                     k_out.data_ptr(), v_out.data_ptr(), None if error_flags is None else error_flags.data_ptr(),
+                     B, Hkv, D, width, NB, 16, block_table.shape[1], code)
+    _call(LIB.attn_gather_paged, "attn_gather_paged", dev, ctypes.byref(p))
+    return k_out, v_out
+
+
+def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens,
+                              scale: float | None = None, max_seq_len: int = 0, num_splits: int = 0, out=None,
+                              lse=None, workspace=None, out_dtype=torch.bfloat16, want_lse: bool = True,
+                              error_flags=None):
+    """:func:`decode_paged` over the block-scaled 8-bit cache of :func:`append_paged`.
+
+    q [B,Hq,D] bf16, D 64 or 128, up to 16 query heads per kv head; the caches
+    E4M3 codes with uint8 scales [num_blocks,Hkv]. Returns ``(O [B,Hq,D], LSE
+    [B,Hq] or None)``.
+    """
+    dev = _same_device(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, out, lse, workspace, error_flags)
+    _need(_pool_checks(k_cache, v_cache, k_scales, v_scales) == ATTN_DTYPE_FP8_E4M3, "E4M3 caches")
+    _check_decode_inputs(q, k_cache, v_cache, block_table, seq_lens)
+    B, Hq, D = q.shape
+    _need(k_cache.shape[3] == D and block_table.shape[0] == B and seq_lens.is_contiguous(), "shapes")
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=out_dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    _need(tuple(out.shape) == (B, Hq, D) and out.is_contiguous(), "out [B, Hq, D]")
+    _need(lse is None or (tuple(lse.shape) == (B, Hq) and lse.is_contiguous() and lse.dtype == torch.float32),
+          "fp32 lse [B, Hq]")
+    p = _decode_params(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, num_splits, out, lse,
+                       error_flags)
+    _call_with_workspace(LIB.attn_decode_paged_block_scaled, "attn_decode_paged_block_scaled", dev, p, k_scales,
+                         v_scales, workspace)
+    return out, lse
+
+
+def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_table, seqlens_k, seqlens_q=None,
+                               scale: float | None = None, causal: bool = True, out=None, lse=None,
+                               out_dtype=torch.bfloat16, want_lse: bool = True, workspace=None, error_flags=None,
+                               cu_seqlens_q=None, max_seqlen_q=None, max_seqlen_k=None):
+    """:func:`prefill_paged` over the block-scaled 8-bit cache of :func:`append_paged`.
+
+    max_seqlen_k (host int) bounds seqlens_k (None: the table's capacity); the
+    workspace grows with it. Returns ``(O, LSE)``.
+    """
+    dev = _same_device(q, k_cache, v_cache, k_scales, v_scales, block_table, seqlens_k, seqlens_q, out, lse,
+                       workspace, error_flags, cu_seqlens_q)
+    _need(_pool_checks(k_cache, v_cache, k_scales, v_scales) == ATTN_DTYPE_FP8_E4M3, "E4M3 caches")
+    NB, Hkv, BS, D = k_cache.shape
+    B = block_table.shape[0]
+    _need(q.shape[-1] == D, "caches of q's head_dim")
+    _need(block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2,
+          "int32 block table [B, max_blocks]")
+    _i32_vec(seqlens_k, B, "seqlens_k")
+    if seqlens_q is not None:
+        _i32_vec(seqlens_q, B, "seqlens_q")
+    p = PrefillParams()
+    out, lse = _queries(p, q, out, lse, out_dtype, want_lse, B, cu_seqlens_q, max_seqlen_q)
+    p.k_cache, p.v_cache, p.block_table = _ptr(k_cache), _ptr(v_cache), _ptr(block_table)
+    p.seqlens_k, p.seqlens_q = _ptr(seqlens_k), _ptr(seqlens_q)
+    p.batch, p.num_kv_heads = B, Hkv
+    p.seqlen_k = block_table.shape[1] * BS if max_seqlen_k is None else int(max_seqlen_k)
+    p.max_blocks_per_seq, p.num_blocks, p.block_size = block_table.shape[1], NB, BS
+    p.scale, p.causal = float(scale if scale is not None else 1.0 / math.sqrt(D)), int(bool(causal))
+    p.error_flags = _ptr(error_flags)
+    _call_with_workspace(LIB.attn_prefill_paged_block_scaled, "attn_prefill_paged_block_scaled", dev, p, k_scales,
+                         v_scales, workspace)
     return out, lse
 
 

@@ -166,6 +166,128 @@ attn_status_t validate_decode(const attn_decode_params* p) {
   return ATTN_OK;
 }
 
+static attn_status_t check_rows(const void* p, int64_t bs, int64_t hs, int64_t rs) {
+  if (!aligned16(p) || !mult8(bs) || !mult8(hs) || !mult8(rs)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+static attn_status_t check_turn(int head_dim, int rotary_dim, float magnitude, const double* inv_freq) {
+  if (head_dim != 64 && head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+  if (rotary_dim < 0 || rotary_dim > head_dim) return ATTN_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (rotary_dim > 0 && !inv_freq) return ATTN_ERR_INVALID_ARG;
+  if (rotary_dim > 0 && !isfinite(magnitude)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static attn_status_t check_pool(int num_blocks, int block_size) {
+  if (block_size != 16) return ATTN_ERR_UNSUPPORTED;
+  if (num_blocks <= 0 || num_blocks > INT32_MAX / 16) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static attn_status_t validate_rotary(const attn_rotary_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->seqlen < 0 || p->num_q_heads <= 0 || (p->k && p->num_k_heads <= 0))
+    return ATTN_ERR_INVALID_ARG;
+  const attn_status_t st = check_turn(p->head_dim, p->rotary_dim, p->magnitude, p->inv_freq);
+  if (st != ATTN_OK) return st;
+  if (p->in_dtype != ATTN_DTYPE_BF16 && p->in_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (p->out_dtype != ATTN_DTYPE_BF16 && p->out_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->seqlen == 0) return ATTN_OK;
+  if (!p->q || !p->q_out || (p->k && !p->k_out)) return ATTN_ERR_INVALID_ARG;
+  // In place, a row is read and written by the same thread only if both views agree.
+  if (p->q == p->q_out && (p->in_dtype != p->out_dtype || p->q_batch_stride != p->qo_batch_stride ||
+                           p->q_head_stride != p->qo_head_stride || p->q_row_stride != p->qo_row_stride))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->k && p->k == p->k_out && (p->in_dtype != p->out_dtype || p->k_batch_stride != p->ko_batch_stride ||
+                                   p->k_head_stride != p->ko_head_stride || p->k_row_stride != p->ko_row_stride))
+    return ATTN_ERR_INVALID_ARG;
+  if (check_rows(p->q, p->q_batch_stride, p->q_head_stride, p->q_row_stride) != ATTN_OK ||
+      check_rows(p->q_out, p->qo_batch_stride, p->qo_head_stride, p->qo_row_stride) != ATTN_OK)
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->k && (check_rows(p->k, p->k_batch_stride, p->k_head_stride, p->k_row_stride) != ATTN_OK ||
+               check_rows(p->k_out, p->ko_batch_stride, p->ko_head_stride, p->ko_row_stride) != ATTN_OK))
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+static attn_status_t validate_plan(const attn_plan_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->batch > 65535 || p->max_blocks_per_seq <= 0 || p->num_free < 0 || p->total_q < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)p->max_blocks_per_seq * 16 > INT32_MAX / 2) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t st = check_pool(p->num_blocks, p->block_size);
+  if (st != ATTN_OK) return st;
+  if (!p->num_used || !p->num_used_out || !p->cu_seqlens_q) return ATTN_ERR_INVALID_ARG;
+  if (p->batch > 0 && (!p->seq_lens || !p->new_lens || !p->block_table || !p->seq_lens_out)) return ATTN_ERR_INVALID_ARG;
+  if (p->num_free > 0 && !p->free_blocks) return ATTN_ERR_INVALID_ARG;
+  if (p->total_q > 0 && (!p->positions || !p->slot_map)) return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static attn_status_t validate_append(const attn_append_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->total < 0 || p->num_kv_heads <= 0 || (p->q && p->num_q_heads <= 0)) return ATTN_ERR_INVALID_ARG;
+  attn_status_t st = check_turn(p->head_dim, p->rotary_dim, p->magnitude, p->inv_freq);
+  if (st != ATTN_OK) return st;
+  st = check_pool(p->num_blocks, p->block_size);
+  if (st != ATTN_OK) return st;
+  if (p->kv_dtype != ATTN_DTYPE_BF16 && p->kv_dtype != ATTN_DTYPE_FP8_E4M3) return ATTN_ERR_INVALID_ARG;
+  if (p->kv_dtype == ATTN_DTYPE_FP8_E4M3 && (!p->k_scales || !p->v_scales)) return ATTN_ERR_INVALID_ARG;
+  if (p->total == 0) return ATTN_OK;
+  if (!p->k || !p->v || !p->k_cache || !p->v_cache || !p->slot_map || (p->q && !p->q_out)) return ATTN_ERR_INVALID_ARG;
+  if (p->rotary_dim > 0 && !p->positions) return ATTN_ERR_INVALID_ARG;
+  if (p->q && p->q == p->q_out && (p->q_row_stride != p->qo_row_stride || p->q_head_stride != p->qo_head_stride))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->k_cache) || !aligned16(p->v_cache) ||
+      check_rows(p->k, 0, p->k_head_stride, p->k_row_stride) != ATTN_OK ||
+      check_rows(p->v, 0, p->v_head_stride, p->v_row_stride) != ATTN_OK)
+    return ATTN_ERR_UNSUPPORTED;
+  if (p->q && (check_rows(p->q, 0, p->q_head_stride, p->q_row_stride) != ATTN_OK ||
+               check_rows(p->q_out, 0, p->qo_head_stride, p->qo_row_stride) != ATTN_OK))
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+static attn_status_t validate_gather(const attn_gather_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->num_kv_heads <= 0 || p->width < 0 || p->max_blocks_per_seq <= 0) return ATTN_ERR_INVALID_ARG;
+  if (p->head_dim != 64 && p->head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_blocks_per_seq * 16 > INT32_MAX / 2 || p->width > INT32_MAX / 2) return ATTN_ERR_INVALID_ARG;
+  const attn_status_t st = check_pool(p->num_blocks, p->block_size);
+  if (st != ATTN_OK) return st;
+  if (p->kv_dtype != ATTN_DTYPE_BF16 && p->kv_dtype != ATTN_DTYPE_FP8_E4M3) return ATTN_ERR_INVALID_ARG;
+  if (p->kv_dtype == ATTN_DTYPE_FP8_E4M3 && (!p->k_scales || !p->v_scales)) return ATTN_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->width == 0) return ATTN_OK;
+  if (!p->k_cache || !p->v_cache || !p->block_table || !p->seq_lens || !p->k_out || !p->v_out)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->k_out) || !aligned16(p->v_out))
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+static attn_status_t validate_decode_block_scaled(const attn_decode_params* p, const uint8_t* k_scales,
+                                                  const uint8_t* v_scales) {
+  if (!p || !k_scales || !v_scales) return ATTN_ERR_INVALID_ARG;
+  if (p->batch < 0 || p->batch > 65535) return ATTN_ERR_INVALID_ARG;
+  if (p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->num_kv_heads > 65535) return ATTN_ERR_INVALID_ARG;
+  if (p->num_q_heads % p->num_kv_heads != 0 || p->num_q_heads / p->num_kv_heads > 16) return ATTN_ERR_UNSUPPORTED;
+  if (p->head_dim != 64 && p->head_dim != 128) return ATTN_ERR_UNSUPPORTED;
+  const attn_status_t st = check_pool(p->num_blocks, p->block_size);
+  if (st != ATTN_OK) return st;
+  if (p->max_blocks_per_seq <= 0 || p->max_seq_len < 0 || p->num_splits < 0) return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)p->max_blocks_per_seq * 16 > INT32_MAX / 2) return ATTN_ERR_INVALID_ARG;
+  if ((int64_t)p->batch * p->num_q_heads > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f) || !isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
+  if (p->o_dtype != ATTN_DTYPE_BF16 && p->o_dtype != ATTN_DTYPE_F32) return ATTN_ERR_INVALID_ARG;
+  if (p->kv_dtype != ATTN_DTYPE_FP8_E4M3) return ATTN_ERR_INVALID_ARG;
+  if (!p->q || !p->k_cache || !p->v_cache || !p->block_table || !p->seq_lens || !p->o) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned16(p->k_cache) || !aligned16(p->v_cache) || !aligned16(p->o))
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 }  // namespace attn
 
 extern "C" {
@@ -192,6 +314,78 @@ attn_status_t attn_decode_paged(const attn_decode_params* p, void* workspace, si
   if (p->batch == 0) return ATTN_OK;
   if (!have_dev) return ATTN_ERR_NO_DEVICE;
   return attn::launch_decode(*p, plan, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t stream) {
+  attn_status_t st = attn::validate_rotary(p);
+  if (st != ATTN_OK) return st;
+  if (p->batch == 0 || p->seqlen == 0) return ATTN_OK;
+  st = attn::check_device();
+  if (st != ATTN_OK) return st;
+  return attn::launch_rotary(*p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_plan_paged_step(const attn_plan_params* p, attn_stream_t stream) {
+  attn_status_t st = attn::validate_plan(p);
+  if (st != ATTN_OK) return st;
+  st = attn::check_device();
+  if (st != ATTN_OK) return st;
+  return attn::launch_plan(*p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_append_paged(const attn_append_params* p, attn_stream_t stream) {
+  attn_status_t st = attn::validate_append(p);
+  if (st != ATTN_OK) return st;
+  if (p->total == 0) return ATTN_OK;
+  st = attn::check_device();
+  if (st != ATTN_OK) return st;
+  return attn::launch_append(*p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_gather_paged(const attn_gather_params* p, attn_stream_t stream) {
+  attn_status_t st = attn::validate_gather(p);
+  if (st != ATTN_OK) return st;
+  if (p->batch == 0 || p->width == 0) return ATTN_OK;
+  st = attn::check_device();
+  if (st != ATTN_OK) return st;
+  return attn::launch_gather(*p, 0, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* p, const uint8_t* k_scales,
+                                             const uint8_t* v_scales, void* workspace, size_t workspace_bytes,
+                                             size_t* workspace_needed, attn_stream_t stream) {
+  attn_status_t st = attn::validate_decode_block_scaled(p, k_scales, v_scales);
+  if (st != ATTN_OK) return st;
+  const bool have_dev = attn::check_device() == ATTN_OK;
+  const attn::DecodePlan plan = attn::plan_decode_block_scaled(*p);
+  if (workspace_needed) *workspace_needed = plan.workspace_bytes;
+  if (workspace == nullptr && workspace_needed != nullptr) return ATTN_OK;  // size query only
+  if (workspace_bytes < plan.workspace_bytes) return ATTN_ERR_WORKSPACE;
+  if (plan.workspace_bytes > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_UNSUPPORTED;
+  if (p->batch == 0) return ATTN_OK;
+  if (!have_dev) return ATTN_ERR_NO_DEVICE;
+  return attn::launch_decode_block_scaled(*p, k_scales, v_scales, plan, workspace,
+                                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status_t attn_prefill_paged_block_scaled(const attn_prefill_params* p, const uint8_t* k_scales,
+                                              const uint8_t* v_scales, void* workspace, size_t workspace_bytes,
+                                              size_t* workspace_needed, attn_stream_t stream) {
+  attn_status_t st = attn::validate_prefill(p);
+  if (st != ATTN_OK) return st;
+  if (!p->k_cache || !k_scales || !v_scales) return ATTN_ERR_INVALID_ARG;
+  st = attn::check_pool(p->num_blocks, p->block_size);
+  if (st != ATTN_OK) return st;
+  if ((int64_t)p->max_blocks_per_seq * 16 > INT32_MAX / 2) return ATTN_ERR_INVALID_ARG;
+  const size_t need = attn::prefill_block_scaled_workspace_bytes(*p);
+  if (workspace_needed) *workspace_needed = need;
+  if (workspace == nullptr && workspace_needed != nullptr) return ATTN_OK;  // size query only
+  if (workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_UNSUPPORTED;
+  if (p->batch == 0 || p->seqlen_q == 0 || (p->cu_seqlens_q && p->total_q == 0)) return ATTN_OK;
+  st = attn::check_device();
+  if (st != ATTN_OK) return st;
+  return attn::launch_prefill_block_scaled(*p, k_scales, v_scales, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 attn_status_t attn_prefill_backward(const attn_backward_params* p, void* workspace, size_t workspace_bytes,

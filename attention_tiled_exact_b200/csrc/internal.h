@@ -121,4 +121,21 @@ CascadePlan plan_cascade(const attn_decode_params& p, int prefix_len);
 attn_status_t launch_cascade(const attn_decode_params& p, const CascadePlan& plan, void* workspace,
                              cudaStream_t stream);
 
+// Rotary positions, the step plan and the paged cache's writer and reader.
+// Arguments were validated by the caller.
+attn_status_t launch_rotary(const attn_rotary_params& p, cudaStream_t stream);
+attn_status_t launch_plan(const attn_plan_params& p, cudaStream_t stream);
+attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream);
+// zero_to: rows behind a sequence are cleared up to the next multiple of this
+// (0: up to width). flag_width: a sequence over width is flagged.
+attn_status_t launch_gather(const attn_gather_params& p, int zero_to, bool flag_width, cudaStream_t stream);
+
+// Attention over the block-scaled 8-bit cache (decode and chunked prefill).
+DecodePlan plan_decode_block_scaled(const attn_decode_params& p);
+attn_status_t launch_decode_block_scaled(const attn_decode_params& p, const uint8_t* k_scales, const uint8_t* v_scales,
+                                         const DecodePlan& plan, void* workspace, cudaStream_t stream);
+size_t prefill_block_scaled_workspace_bytes(const attn_prefill_params& p);
+attn_status_t launch_prefill_block_scaled(const attn_prefill_params& p, const uint8_t* k_scales,
+                                          const uint8_t* v_scales, void* workspace, cudaStream_t stream);
+
 }  // namespace attn

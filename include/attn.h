@@ -69,6 +69,7 @@ typedef enum { ATTN_DTYPE_BF16 = 0, ATTN_DTYPE_F32 = 1, ATTN_DTYPE_FP8_E4M3 = 2 
 #define ATTN_FAULT_BAD_BLOCK 0x2    /* a block-table entry was outside [0, num_blocks) */
 #define ATTN_FAULT_BAD_LENGTH 0x4   /* a sequence length exceeded its block table or was negative */
 #define ATTN_FAULT_PREFIX_MISMATCH 0x8 /* attn_decode_paged_shared_prefix: a table row's prefix blocks differ from row 0's */
+#define ATTN_FAULT_NO_BLOCK 0x20    /* attn_plan_paged_step: the free list ran out of blocks */
 #define ATTN_FAULT_BOUNDS 0x10      /* debug build only: an index failed its bounds check (site in bits 16..23) */
 /* The site (attn_bounds_site_t) of the first failed bounds check of a debug
  * build, 0 if none; the word's other bits are the ATTN_FAULT_* flags. */
@@ -539,6 +540,197 @@ ATTN_API attn_status_t attn_decode_graph_pool_create(const attn_decode_params* p
 ATTN_API attn_status_t attn_decode_graph_pool_replay(attn_decode_graph_pool* pool, int32_t batch, int32_t max_seq_len,
                                                      attn_stream_t stream, int32_t* bucket_batch, int32_t* bucket_len);
 ATTN_API void attn_decode_graph_pool_destroy(attn_decode_graph_pool* pool);
+
+/*
+ * Rotary positions. Pair i (0 <= i < rotary_dim / 2) of a row at position p is
+ * turned by the angle a = p * inv_freq[i] and scaled by magnitude m:
+ *   (x1, x2) -> m (x1 cos a - x2 sin a,  x2 cos a + x1 sin a)
+ * The pair is (x[i], x[i + rotary_dim / 2]) in the half layout (interleaved ==
+ * 0) and (x[2 i], x[2 i + 1]) in the interleaved one; elements from rotary_dim
+ * on are copied. inv_freq (device, fp64, [rotary_dim / 2]) holds the angle of
+ * each pair per position in radians, so every scaling for long contexts that
+ * acts on the frequencies is a choice of inv_freq and m. The angle is reduced
+ * in 64 bits and the turn is computed in fp32: positions up to 2^31 - 1 keep
+ * the accuracy of near ones.
+ * inverse != 0 turns by -a: the transpose of the map, which is its gradient
+ * (attn_rotary of dQ / dK with inverse gives the gradients of the unrotated
+ * q / k).
+ *
+ * Two tensors of the same rows are turned by one launch; k may be NULL (then
+ * num_k_heads is ignored). q [batch, num_q_heads, seqlen, head_dim], k [batch,
+ * num_k_heads, seqlen, head_dim], outputs alike, element strides, head_dim
+ * contiguous; packed [total, heads, head_dim] rows are batch = 1, seqlen =
+ * total with their strides. An output may be its input (in place); any other
+ * overlap is not allowed. positions (device, [batch, seqlen] int32,
+ * contiguous; NULL: row s has position s): a row with a negative position is
+ * not written.
+ * Requirements: head_dim 64 or 128; rotary_dim a multiple of 16, at most
+ * head_dim; in_dtype / out_dtype BF16 or F32; pointers 16-byte aligned and
+ * strides multiples of 8 elements.
+ */
+typedef struct {
+  const void* q;
+  const void* k; /* nullable */
+  void* q_out;
+  void* k_out;
+  const int32_t* positions; /* nullable */
+  const double* inv_freq;
+  int batch, num_q_heads, num_k_heads, seqlen, head_dim;
+  int rotary_dim, interleaved, inverse;
+  float magnitude;
+  attn_dtype_t in_dtype, out_dtype;
+  int64_t q_batch_stride, q_head_stride, q_row_stride;
+  int64_t k_batch_stride, k_head_stride, k_row_stride;
+  int64_t qo_batch_stride, qo_head_stride, qo_row_stride;
+  int64_t ko_batch_stride, ko_head_stride, ko_row_stride;
+} attn_rotary_params;
+
+ATTN_API attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t stream);
+
+/*
+ * The plan of one step over a paged cache, built on the device: sequence b
+ * holds seq_lens[b] cached tokens and adds new_lens[b] (0 is allowed). It
+ * keeps the ceil(seq_lens / 16) blocks its table row lists already and takes
+ * the further blocks it needs from the free list, in sequence order:
+ * free_blocks[num_used[0] ...]. Outputs:
+ *   block_table  the new entries, from column ceil(seq_lens[b] / 16) on
+ *   seq_lens_out [batch] seq_lens + new_lens
+ *   cu_seqlens_q [batch + 1] prefix sums of new_lens (the packed rows)
+ *   positions    [total_q] each new token's position in its sequence
+ *   slot_map     [total_q] its slot: block * 16 + position % 16
+ *   num_used_out [1] num_used plus the blocks taken
+ * Rows of positions / slot_map behind cu_seqlens_q[batch] get -1, which
+ * attn_rotary and attn_append_paged skip: a captured step may be sized for
+ * more rows than it has. seq_lens_out may be seq_lens and num_used_out may be
+ * num_used (the state advances in place, so a captured step can be replayed);
+ * other outputs overlap nothing.
+ * Faults (error_flags): ATTN_FAULT_BAD_LENGTH for a negative length, a
+ * sequence over max_blocks_per_seq * 16 tokens or more than total_q new
+ * tokens (the new tokens past either bound are dropped: no row, no block, and
+ * seq_lens_out and num_used_out do not count them); ATTN_FAULT_NO_BLOCK when the free list runs out and
+ * ATTN_FAULT_BAD_BLOCK for an id outside [0, num_blocks): the entry and its
+ * tokens' slots are then -1.
+ * Requirements: block_size == 16, num_blocks * 16 <= 2^31 - 1, batch <= 65535.
+ */
+typedef struct {
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  int32_t* block_table;
+  const int32_t* free_blocks;
+  const int32_t* num_used;
+  int32_t* seq_lens_out;
+  int32_t* cu_seqlens_q;
+  int32_t* positions;
+  int32_t* slot_map;
+  int32_t* num_used_out;
+  int32_t* error_flags; /* nullable */
+  int batch, max_blocks_per_seq, num_blocks, num_free, total_q, block_size;
+} attn_plan_params;
+
+ATTN_API attn_status_t attn_plan_paged_step(const attn_plan_params* p, attn_stream_t stream);
+
+/*
+ * The block-scaled 8-bit cache. k_cache / v_cache [num_blocks, num_kv_heads,
+ * 16, head_dim] hold OCP E4M3 codes, and k_scales / v_scales [num_blocks,
+ * num_kv_heads] hold one exponent byte for each block and head (E8M0: scale =
+ * 2^(byte - 127), 255 = NaN); the cached element is code * scale. A scale is a
+ * power of two because E4M3 is a floating type: the element keeps its 4
+ * significant bits whatever the scale, code * scale is exact in bf16, and a
+ * block whose scale has to grow later re-codes its tokens without a second
+ * rounding (but for codes that become subnormal).
+ *
+ * attn_append_paged: rotates the new tokens' queries and keys (as attn_rotary)
+ * and writes the keys and values into the pages, all in one launch. Row t of
+ * k and v goes to slot_map[t] (block * 16 + offset); a negative slot is a row
+ * without a token: nothing of it is written (its q row neither). With
+ * rotary_dim == 0 nothing is rotated (positions and inv_freq are ignored);
+ * q == NULL leaves the queries out.
+ * kv_dtype BF16: the pages hold bf16 elements; slots may come in any order.
+ * kv_dtype FP8_E4M3: the new tokens of a block must be consecutive rows with
+ * ascending consecutive slots (a step's rows are, see attn_plan_paged_step),
+ * and a block may be written by one such run per call. The run replaces the
+ * block from its first slot on: the tokens in front of it are kept, whatever
+ * is behind it is not. The block's scale is then 2^e with the smallest e in
+ * [-110, 120] for which every kept and new finite element is within 448 * 2^e;
+ * kept tokens are re-coded if it changed. Rounding is to nearest even; an
+ * element that is NaN or infinite is stored as NaN.
+ * A slot >= num_blocks * 16 is skipped and flagged (ATTN_FAULT_BAD_BLOCK).
+ * Layout: q, q_out [total, num_q_heads, head_dim], k, v [total, num_kv_heads,
+ * head_dim] bf16 with element strides; q_out may be q. Requirements as
+ * attn_rotary, block_size == 16, num_blocks * 16 <= 2^31 - 1.
+ */
+typedef struct {
+  const void* q; /* nullable */
+  void* q_out;
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  uint8_t* k_scales; /* FP8_E4M3 only */
+  uint8_t* v_scales;
+  const int32_t* slot_map;
+  const int32_t* positions;
+  const double* inv_freq;
+  int32_t* error_flags; /* nullable */
+  int total, num_q_heads, num_kv_heads, head_dim;
+  int num_blocks, block_size;
+  int rotary_dim, interleaved;
+  float magnitude;
+  attn_dtype_t kv_dtype;
+  int64_t q_row_stride, q_head_stride, qo_row_stride, qo_head_stride;
+  int64_t k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+} attn_append_params;
+
+ATTN_API attn_status_t attn_append_paged(const attn_append_params* p, attn_stream_t stream);
+
+/*
+ * The pages' values back as dense bf16: k_out, v_out [batch, num_kv_heads,
+ * width, head_dim] contiguous; row t of sequence b is its cached token t, rows
+ * from seq_lens[b] on are 0. Exact for both cache types (an element too large
+ * for bf16 becomes infinite). A sequence longer than width or than its table
+ * is cut there (the latter flagged ATTN_FAULT_BAD_LENGTH); a table entry
+ * outside the pool gives rows of 0 (ATTN_FAULT_BAD_BLOCK).
+ */
+typedef struct {
+  const void* k_cache;
+  const void* v_cache;
+  const uint8_t* k_scales; /* FP8_E4M3 only */
+  const uint8_t* v_scales;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  void* k_out;
+  void* v_out;
+  int32_t* error_flags; /* nullable */
+  int batch, num_kv_heads, head_dim, width;
+  int num_blocks, block_size, max_blocks_per_seq;
+  attn_dtype_t kv_dtype;
+} attn_gather_params;
+
+ATTN_API attn_status_t attn_gather_paged(const attn_gather_params* p, attn_stream_t stream);
+
+/*
+ * attn_decode_paged over the block-scaled 8-bit cache: p as there with
+ * kv_dtype == ATTN_DTYPE_FP8_E4M3 (k_scale / v_scale are ignored), head_dim 64
+ * or 128 and any num_q_heads / num_kv_heads from 1 to 16. Same workspace
+ * protocol; the size depends on the device's SM count. Scales of the blocks of
+ * one sequence and head may differ by up to 2^100.
+ */
+ATTN_API attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* p, const uint8_t* k_scales,
+                                                      const uint8_t* v_scales, void* workspace,
+                                                      size_t workspace_bytes, size_t* workspace_needed,
+                                                      attn_stream_t stream);
+
+/*
+ * attn_prefill over the block-scaled 8-bit cache (chunked prefill): p as for
+ * the paged mode of attn_prefill (padded or packed queries), k_cache / v_cache
+ * holding E4M3 codes. p->seqlen_k bounds seqlens_k: a longer sequence is cut
+ * there and flagged (ATTN_FAULT_BAD_LENGTH). Workspace protocol as
+ * attn_decode_paged.
+ */
+ATTN_API attn_status_t attn_prefill_paged_block_scaled(const attn_prefill_params* p, const uint8_t* k_scales,
+                                                       const uint8_t* v_scales, void* workspace,
+                                                       size_t workspace_bytes, size_t* workspace_needed,
+                                                       attn_stream_t stream);
 
 /*
  * Split-KV log-sum-exp combine ("GPU Kernel 调度:大模型推理的拐点 2026",
