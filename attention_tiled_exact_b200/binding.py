@@ -679,40 +679,63 @@ def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, out, lse=No
 # ----------------------------------------------------------------------------
 
 
-def _same_device(*tensors):
-    """The one CUDA device of the tensors that are given."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        _need(t.is_cuda and (dev is None or t.device == dev), "CUDA tensors of one device")
-        dev = t.device
-    return dev
+# A step of a few tokens runs for a few microseconds on the GPU, so these calls
+# are written for the host's time: one struct constructor, no formatted messages
+# before a failure, and the raw stream and device numbers.
 
 
-def _call(fn, where, device, *args):
-    """fn(*args, stream) on the device's current stream, with that device current."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(device)), where)
+def _device_index(first, *others) -> int:
+    """The number of the one CUDA device of the tensors that are given (None: left out)."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("CUDA tensors of one device")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError("CUDA tensors of one device")
+    return index
+
+
+def _call(fn, where, index, *args):
+    """fn(*args, stream) on the current stream of device ``index``, with that device current."""
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, _stream(device)), where)
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != ATTN_OK:
+        raise AttnError(status, where)
 
 
-def _call_with_workspace(fn, where, device, p, k_scales, v_scales, workspace):
-    """Query the workspace size, take the caller's or a new one, and launch."""
-    with torch.cuda.device(device):
-        ref, need = ctypes.byref(p), ctypes.c_size_t(0)
-        _check(fn(ref, _ptr(k_scales), _ptr(v_scales), None, 0, ctypes.byref(need), None), where + "(size)")
-        if workspace is None and need.value > 0:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-        ws_ptr = _ptr(workspace) if workspace is not None else ctypes.c_void_p(0)
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-        _check(fn(ref, _ptr(k_scales), _ptr(v_scales), ws_ptr, ws_bytes, None, _stream(device)), where)
+def _call_with_workspace(fn, where, index, p, k_scales, v_scales, workspace):
+    """Query the workspace size, take the caller's workspace or a new one, and launch."""
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _call_with_workspace(fn, where, index, p, k_scales, v_scales, workspace)
+    ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+    if workspace is None:
+        need = ctypes.c_size_t(0)
+        _check(fn(p, ks, vs, None, 0, need, None), where)
+        if need.value:
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=k_scales.device)
+    if workspace is None:
+        ptr, size = None, 0
+    else:
+        ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(fn(p, ks, vs, ptr, size, None, torch._C._cuda_getCurrentRawStream(index)), where)
 
 
 def _i32_vec(t, n, what):
-    _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n, f"int32 {what} [{n}]")
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"int32 {what} [{n}]")
+
+
+def _table(t, batch):
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != batch or not t.is_contiguous():
+        raise ValueError("int32 block table [B, max_blocks]")
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, total_q: int, num_blocks: int,
@@ -731,42 +754,56 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     Returns ``(seq_lens_out [B], cu_seqlens_q [B + 1], positions [total_q],
     slot_map [total_q], num_used_out [1])``.
     """
-    dev = _same_device(seq_lens, new_lens, block_table, free_blocks, num_used, seq_lens_out, cu_seqlens_q, positions,
-                       slot_map, num_used_out, error_flags)
+    index = _device_index(seq_lens, new_lens, block_table, free_blocks, num_used, seq_lens_out, cu_seqlens_q,
+                          positions, slot_map, num_used_out, error_flags)
     B, total_q = seq_lens.numel(), int(total_q)
-    _need(total_q >= 0, "total_q >= 0")
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.dtype == torch.int32 and
-          block_table.is_contiguous(), "int32 block table [B, max_blocks]")
-    _need(free_blocks.dtype == torch.int32 and free_blocks.is_contiguous(), "int32 free_blocks")
-
-    def out(t, n):
-        return torch.empty(n, dtype=torch.int32, device=dev) if t is None else t
-    seq_lens_out, cu_seqlens_q, num_used_out = out(seq_lens_out, B), out(cu_seqlens_q, B + 1), out(num_used_out, 1)
-    positions, slot_map = out(positions, total_q), out(slot_map, total_q)
-    for t, n, what in ((seq_lens, B, "seq_lens"), (new_lens, B, "new_lens"), (num_used, 1, "num_used"),
-                       (seq_lens_out, B, "seq_lens_out"), (cu_seqlens_q, B + 1, "cu_seqlens_q"),
-                       (num_used_out, 1, "num_used_out"), (positions, total_q, "positions"),
-                       (slot_map, total_q, "slot_map")):
-        _i32_vec(t, n, what)
+    if total_q < 0:
+        raise ValueError("total_q >= 0")
+    _table(block_table, B)
+    num_free = free_blocks.numel()
+    _i32_vec(free_blocks, num_free, "free_blocks")
+    new = seq_lens.new_empty
+    if seq_lens_out is None:
+        seq_lens_out = new(B, dtype=torch.int32)
+    if cu_seqlens_q is None:
+        cu_seqlens_q = new(B + 1, dtype=torch.int32)
+    if positions is None:
+        positions = new(total_q, dtype=torch.int32)
+    if slot_map is None:
+        slot_map = new(total_q, dtype=torch.int32)
+    if num_used_out is None:
+        num_used_out = new(1, dtype=torch.int32)
+    _i32_vec(seq_lens, B, "seq_lens")
+    _i32_vec(new_lens, B, "new_lens")
+    _i32_vec(num_used, 1, "num_used")
+    _i32_vec(seq_lens_out, B, "seq_lens_out")
+    _i32_vec(cu_seqlens_q, B + 1, "cu_seqlens_q")
+    _i32_vec(positions, total_q, "positions")
+    _i32_vec(slot_map, total_q, "slot_map")
+    _i32_vec(num_used_out, 1, "num_used_out")
     p = PlanParams(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
                    num_used.data_ptr(), seq_lens_out.data_ptr(), cu_seqlens_q.data_ptr(), positions.data_ptr(),
-                   slot_map.data_ptr(), num_used_out.data_ptr(),
-                   None if error_flags is None else error_flags.data_ptr(), B, block_table.shape[1], int(num_blocks),
-                   free_blocks.numel(), total_q, 16)
-    _call(LIB.attn_plan_paged_step, "attn_plan_paged_step", dev, ctypes.byref(p))
+                   slot_map.data_ptr(), num_used_out.data_ptr(), _opt(error_flags), B, block_table.shape[1],
+                   int(num_blocks), num_free, total_q, 16)
+    _call(LIB.attn_plan_paged_step, "attn_plan_paged_step", index, p)
     return seq_lens_out, cu_seqlens_q, positions, slot_map, num_used_out
 
 
-def _in_code(dtype) -> int:
-    if dtype == torch.bfloat16:
-        return ATTN_DTYPE_BF16
-    _need(dtype == torch.float32, "bfloat16 or float32 rows")
-    return ATTN_DTYPE_F32
+_ROW_CODES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float32: ATTN_DTYPE_F32}
 
 
-def _turn_checks(inv_freq):
-    _need(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous(),
-          "float64 inv_freq [rotary_dim / 2]")
+def _row_code(dtype) -> int:
+    code = _ROW_CODES.get(dtype)
+    if code is None:
+        raise ValueError("bfloat16 or float32 rows")
+    return code
+
+
+def _frequencies(inv_freq) -> int:
+    """Checks inv_freq; returns rotary_dim."""
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("float64 inv_freq [rotary_dim / 2]")
+    return 2 * inv_freq.numel()
 
 
 def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: bool = False, magnitude: float = 1.0,
@@ -783,55 +820,64 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: b
     turns back: of dQ, dK it gives the gradients of the unrotated q, k.
     q_out / k_out may be q / k. Returns ``(q_out, k_out)``.
     """
-    packed = q.dim() == 3
-    _need(packed or q.dim() == 4, "q must be [B, Hq, S, D] or packed [T, Hq, D]")
-    dev = _same_device(q, k, inv_freq, positions, q_out, k_out)
-    _turn_checks(inv_freq)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=dev)
-    if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=out_dtype or k.dtype, device=dev)
+    index = _device_index(q, k, inv_freq, positions, q_out, k_out)
+    rotary_dim = _frequencies(inv_freq)
+    shape = q.shape
+    packed = len(shape) == 3
     if packed:
-        B, (S, Hq, D) = 1, q.shape
+        S, Hq, D = shape
+        B = 1
+    elif len(shape) == 4:
+        B, Hq, S, D = shape
     else:
-        B, Hq, S, D = q.shape
-    views = []
-    for x, y in ((q, q_out), (k, k_out)):
-        if x is None:
-            views.append((0, 0, 0, 0, 0, 0))
-            continue
-        _need(x.dim() == q.dim() and x.shape[-1] == D and y.shape == x.shape and
-              ((x.shape[0] == S) if packed else (x.shape[0] == B and x.shape[2] == S)), "shapes of q, k and outputs")
-        _need(x.stride(-1) == 1 and y.stride(-1) == 1, "last dim contiguous")
-        xs, ys = x.stride(), y.stride()
-        views.append((0, xs[1], xs[0], 0, ys[1], ys[0]) if packed else (*xs[:3], *ys[:3]))
-    if k is not None:
-        _need(k.dtype == q.dtype and k_out.dtype == q_out.dtype, "one dtype for q and k")
+        raise ValueError("q must be [B, Hq, S, D] or packed [T, Hq, D]")
+    if q_out is None:
+        q_out = q.new_empty(shape, dtype=out_dtype)
+    xs, ys = q.stride(), q_out.stride()
+    if q_out.shape != shape or xs[-1] != 1 or ys[-1] != 1:
+        raise ValueError("q_out of q's shape; last dims contiguous")
+    qv, qo = ((0, xs[1], xs[0]), (0, ys[1], ys[0])) if packed else (xs[:3], ys[:3])
+    in_code, out_code = _row_code(q.dtype), _row_code(q_out.dtype)
+    if k is None:
+        Hk, k_ptr, ko_ptr, kv, ko = 0, None, None, (0, 0, 0), (0, 0, 0)
+    else:
+        kshape = k.shape
+        if k_out is None:
+            k_out = k.new_empty(kshape, dtype=out_dtype)
+        xs, ys = k.stride(), k_out.stride()
+        if len(kshape) != len(shape) or kshape[-1] != D or kshape[0] != shape[0] or (not packed and kshape[2] != S):
+            raise ValueError("k of q's rows and head_dim")
+        if k_out.shape != kshape or xs[-1] != 1 or ys[-1] != 1:
+            raise ValueError("k_out of k's shape; last dims contiguous")
+        if k.dtype is not q.dtype or k_out.dtype is not q_out.dtype:
+            raise ValueError("one dtype for q and k")
+        kv, ko = ((0, xs[1], xs[0]), (0, ys[1], ys[0])) if packed else (xs[:3], ys[:3])
+        Hk, k_ptr, ko_ptr = kshape[1], k.data_ptr(), k_out.data_ptr()
     if positions is not None:
         _i32_vec(positions, B * S, "positions")
-    Hk = 0 if k is None else k.shape[1]
-    (qb, qh, qr, ob, oh, orow), (kb, kh, kr, pb, ph, pr) = views
-    p = RotaryParams(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                     None if k is None else k_out.data_ptr(), None if positions is None else positions.data_ptr(),
-                     inv_freq.data_ptr(), B, Hq, Hk, S, D, 2 * inv_freq.numel(), int(bool(interleaved)),
-                     int(bool(inverse)), float(magnitude), _in_code(q.dtype), _in_code(q_out.dtype),
-                     qb, qh, qr, kb, kh, kr, ob, oh, orow, pb, ph, pr)
-    _call(LIB.attn_rotary, "attn_rotary", dev, ctypes.byref(p))
+    p = RotaryParams(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, _opt(positions), inv_freq.data_ptr(), B, Hq, Hk,
+                     S, D, rotary_dim, 1 if interleaved else 0, 1 if inverse else 0, magnitude, in_code, out_code,
+                     *qv, *kv, *qo, *ko)
+    _call(LIB.attn_rotary, "attn_rotary", index, p)
     return q_out, k_out
 
 
-def _pool_checks(k_cache, v_cache, k_scales, v_scales):
-    """Shape and dtype checks of a paged cache; returns its dtype code."""
-    _need(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and k_cache.shape[2] == 16,
-          "caches [num_blocks, Hkv, 16, D]")
-    _need(k_cache.is_contiguous() and v_cache.is_contiguous() and k_cache.dtype == v_cache.dtype, "contiguous caches")
-    if k_cache.dtype == torch.bfloat16:
-        return ATTN_DTYPE_BF16
-    _need(_is_fp8(k_cache), "bf16 or E4M3 caches")
+def _pool(k_cache, v_cache, k_scales, v_scales):
+    """Checks a paged cache; returns (num_blocks, Hkv, D, dtype code)."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or shape[2] != 16 or v_cache.shape != shape or v_cache.dtype is not dtype:
+        raise ValueError("k_cache and v_cache [num_blocks, Hkv, 16, D] of one dtype")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("contiguous caches")
+    NB, Hkv, _, D = shape
+    if dtype is torch.bfloat16:
+        return NB, Hkv, D, ATTN_DTYPE_BF16
+    if dtype is not torch.uint8 and dtype is not torch.float8_e4m3fn:
+        raise ValueError("bf16 or E4M3 caches")
     for t in (k_scales, v_scales):
-        _need(t is not None and t.dtype == torch.uint8 and t.is_contiguous() and
-              tuple(t.shape) == tuple(k_cache.shape[:2]), "uint8 scales [num_blocks, Hkv]")
-    return ATTN_DTYPE_FP8_E4M3
+        if t is None or t.dtype is not torch.uint8 or t.shape != shape[:2] or not t.is_contiguous():
+            raise ValueError("uint8 scales [num_blocks, Hkv]")
+    return NB, Hkv, D, ATTN_DTYPE_FP8_E4M3
 
 
 def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None, q=None, inv_freq=None, positions=None,
@@ -848,39 +894,42 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
     of :func:`rotary`; the keys are turned, and so are the queries q [T,Hq,D].
     Returns the turned queries (q_out, which may be q), or None without q.
     """
-    dev = _same_device(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, q, inv_freq, positions, q_out, error_flags)
-    code = _pool_checks(k_cache, v_cache, k_scales, v_scales)
-    NB, Hkv, _, D = k_cache.shape
-    _need(k.dim() == 3 and v.shape == k.shape and tuple(k.shape[1:]) == (Hkv, D), "k, v [T, Hkv, D]")
-    T = k.shape[0]
-    _need(k.dtype == v.dtype == torch.bfloat16 and k.stride(2) == 1 and v.stride(2) == 1,
-          "bf16 k, v, last dim contiguous")
+    index = _device_index(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, q, inv_freq, positions, q_out,
+                          error_flags)
+    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    shape, ks, vs = k.shape, k.stride(), v.stride()
+    if len(shape) != 3 or v.shape != shape or shape[1] != Hkv or shape[2] != D:
+        raise ValueError("k, v [T, Hkv, D]")
+    T = shape[0]
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or ks[2] != 1 or vs[2] != 1:
+        raise ValueError("bf16 k, v, last dim contiguous")
     _i32_vec(slot_map, T, "slot_map")
-    p = AppendParams()
-    if q is not None:
-        _need(q.dim() == 3 and q.shape[0] == T and q.shape[2] == D and q.dtype == torch.bfloat16 and q.stride(2) == 1,
-              "bf16 q [T, Hq, D], last dim contiguous")
+    if q is None:
+        q_out, q_ptr, qo_ptr, Hq, qs, qo = None, None, None, 0, (0, 0), (0, 0)
+    else:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype is not torch.bfloat16:
+            raise ValueError("bf16 q [T, Hq, D]")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        _need(q_out.shape == q.shape and q_out.dtype == q.dtype and q_out.stride(2) == 1, "q_out like q")
-        p.q, p.q_out, p.num_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-        p.q_row_stride, p.q_head_stride, _ = q.stride()
-        p.qo_row_stride, p.qo_head_stride, _ = q_out.stride()
-    if inv_freq is not None:
-        _turn_checks(inv_freq)
-        _need(positions is not None, "positions of the rows to turn")
+            q_out = q.new_empty(q.shape)
+        qs, qo = q.stride(), q_out.stride()
+        if q_out.shape != q.shape or q_out.dtype is not q.dtype or qs[2] != 1 or qo[2] != 1:
+            raise ValueError("q_out like q; last dims contiguous")
+        q_ptr, qo_ptr, Hq = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+    if inv_freq is None:
+        rotary_dim, pos_ptr, freq_ptr = 0, None, None
+    else:
+        rotary_dim = _frequencies(inv_freq)
+        if positions is None:
+            raise ValueError("positions of the rows to turn")
         _i32_vec(positions, T, "positions")
-        p.inv_freq, p.positions, p.rotary_dim = inv_freq.data_ptr(), positions.data_ptr(), 2 * inv_freq.numel()
-        p.interleaved, p.magnitude = int(bool(interleaved)), float(magnitude)
-    p.k, p.v, p.k_cache, p.v_cache = k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
-    if code == ATTN_DTYPE_FP8_E4M3:
-        p.k_scales, p.v_scales = k_scales.data_ptr(), v_scales.data_ptr()
-    p.slot_map, p.error_flags = slot_map.data_ptr(), None if error_flags is None else error_flags.data_ptr()
-    p.total, p.num_kv_heads, p.head_dim, p.num_blocks, p.block_size, p.kv_dtype = T, Hkv, D, NB, 16, code
-    p.k_row_stride, p.k_head_stride, _ = k.stride()
-    p.v_row_stride, p.v_head_stride, _ = v.stride()
-    _call(LIB.attn_append_paged, "attn_append_paged", dev, ctypes.byref(p))
-    return q_out if q is not None else None
+        pos_ptr, freq_ptr = positions.data_ptr(), inv_freq.data_ptr()
+    fp8 = code == ATTN_DTYPE_FP8_E4M3
+    p = AppendParams(q_ptr, qo_ptr, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                     k_scales.data_ptr() if fp8 else None, v_scales.data_ptr() if fp8 else None, slot_map.data_ptr(),
+                     pos_ptr, freq_ptr, _opt(error_flags), T, Hq, Hkv, D, NB, 16, rotary_dim, 1 if interleaved else 0,
+                     magnitude, code, qs[0], qs[1], qo[0], qo[1], ks[0], ks[1], vs[0], vs[1])
+    _call(LIB.attn_append_paged, "attn_append_paged", index, p)
+    return q_out
 
 
 def gather_paged(k_cache, v_cache, block_table, seq_lens, width: int, k_scales=None, v_scales=None, k_out=None,
@@ -890,26 +939,27 @@ def gather_paged(k_cache, v_cache, block_table, seq_lens, width: int, k_scales=N
     The caches and scales are those of :func:`append_paged`; rows from
     seq_lens[b] on are 0.
     """
-    dev = _same_device(k_cache, v_cache, block_table, seq_lens, k_scales, v_scales, k_out, v_out, error_flags)
-    code = _pool_checks(k_cache, v_cache, k_scales, v_scales)
-    NB, Hkv, _, D = k_cache.shape
-    B, width = block_table.shape[0], int(width)
-    _need(block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2,
-          "int32 block table [B, max_blocks]")
+    index = _device_index(k_cache, v_cache, block_table, seq_lens, k_scales, v_scales, k_out, v_out, error_flags)
+    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    B, width = seq_lens.numel(), int(width)
+    _table(block_table, B)
     _i32_vec(seq_lens, B, "seq_lens")
-    _need(width >= 0, "width >= 0")
+    if width < 0:
+        raise ValueError("width >= 0")
+    shape = (B, Hkv, width, D)
     if k_out is None:
-        k_out = torch.empty((B, Hkv, width, D), dtype=torch.bfloat16, device=dev)
+        k_out = k_cache.new_empty(shape, dtype=torch.bfloat16)
     if v_out is None:
-        v_out = torch.empty((B, Hkv, width, D), dtype=torch.bfloat16, device=dev)
+        v_out = k_cache.new_empty(shape, dtype=torch.bfloat16)
     for t in (k_out, v_out):
-        _need(tuple(t.shape) == (B, Hkv, width, D) and t.dtype == torch.bfloat16 and t.is_contiguous(),
-              "contiguous bf16 outputs [B, Hkv, width, D]")
-    scales = (k_scales.data_ptr(), v_scales.data_ptr()) if code == ATTN_DTYPE_FP8_E4M3 else (None, None)
-    p = GatherParams(k_cache.data_ptr(), v_cache.data_ptr(), *scales, block_table.data_ptr(), seq_lens.data_ptr(),
-                     k_out.data_ptr(), v_out.data_ptr(), None if error_flags is None else error_flags.data_ptr(),
-                     B, Hkv, D, width, NB, 16, block_table.shape[1], code)
-    _call(LIB.attn_gather_paged, "attn_gather_paged", dev, ctypes.byref(p))
+        if t.shape != shape or t.dtype is not torch.bfloat16 or not t.is_contiguous():
+            raise ValueError("contiguous bf16 outputs [B, Hkv, width, D]")
+    fp8 = code == ATTN_DTYPE_FP8_E4M3
+    p = GatherParams(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None,
+                     v_scales.data_ptr() if fp8 else None, block_table.data_ptr(), seq_lens.data_ptr(),
+                     k_out.data_ptr(), v_out.data_ptr(), _opt(error_flags), B, Hkv, D, width, NB, 16,
+                     block_table.shape[1], code)
+    _call(LIB.attn_gather_paged, "attn_gather_paged", index, p)
     return k_out, v_out
 
 
@@ -923,21 +973,30 @@ def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tab
     E4M3 codes with uint8 scales [num_blocks,Hkv]. Returns ``(O [B,Hq,D], LSE
     [B,Hq] or None)``.
     """
-    dev = _same_device(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, out, lse, workspace, error_flags)
-    _need(_pool_checks(k_cache, v_cache, k_scales, v_scales) == ATTN_DTYPE_FP8_E4M3, "E4M3 caches")
-    _check_decode_inputs(q, k_cache, v_cache, block_table, seq_lens)
-    B, Hq, D = q.shape
-    _need(k_cache.shape[3] == D and block_table.shape[0] == B and seq_lens.is_contiguous(), "shapes")
+    index = _device_index(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, out, lse, workspace,
+                          error_flags)
+    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    if code != ATTN_DTYPE_FP8_E4M3:
+        raise ValueError("E4M3 caches")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("contiguous bf16 q [B, Hq, D]")
+    B, Hq, _ = shape
+    _table(block_table, B)
+    _i32_vec(seq_lens, B, "seq_lens")
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    _need(tuple(out.shape) == (B, Hq, D) and out.is_contiguous(), "out [B, Hq, D]")
-    _need(lse is None or (tuple(lse.shape) == (B, Hq) and lse.is_contiguous() and lse.dtype == torch.float32),
-          "fp32 lse [B, Hq]")
-    p = _decode_params(q, k_cache, v_cache, block_table, seq_lens, scale, max_seq_len, num_splits, out, lse,
-                       error_flags)
-    _call_with_workspace(LIB.attn_decode_paged_block_scaled, "attn_decode_paged_block_scaled", dev, p, k_scales,
+        out = q.new_empty(shape, dtype=out_dtype)
+    elif out.shape != shape or not out.is_contiguous():
+        raise ValueError("contiguous out [B, Hq, D]")
+    if lse is None:
+        lse = q.new_empty((B, Hq), dtype=torch.float32) if want_lse else None
+    elif lse.shape != shape[:2] or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        raise ValueError("contiguous fp32 lse [B, Hq]")
+    p = DecodeParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                     out.data_ptr(), _opt(lse), B, Hq, Hkv, D, 16, block_table.shape[1], NB, int(max_seq_len),
+                     int(num_splits), 1.0 / math.sqrt(D) if scale is None else scale, _row_code(out.dtype),
+                     _opt(error_flags), code, 1.0, 1.0)
+    _call_with_workspace(LIB.attn_decode_paged_block_scaled, "attn_decode_paged_block_scaled", index, p, k_scales,
                          v_scales, workspace)
     return out, lse
 
@@ -951,27 +1010,28 @@ def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_ta
     max_seqlen_k (host int) bounds seqlens_k (None: the table's capacity); the
     workspace grows with it. Returns ``(O, LSE)``.
     """
-    dev = _same_device(q, k_cache, v_cache, k_scales, v_scales, block_table, seqlens_k, seqlens_q, out, lse,
-                       workspace, error_flags, cu_seqlens_q)
-    _need(_pool_checks(k_cache, v_cache, k_scales, v_scales) == ATTN_DTYPE_FP8_E4M3, "E4M3 caches")
-    NB, Hkv, BS, D = k_cache.shape
-    B = block_table.shape[0]
-    _need(q.shape[-1] == D, "caches of q's head_dim")
-    _need(block_table.dtype == torch.int32 and block_table.is_contiguous() and block_table.dim() == 2,
-          "int32 block table [B, max_blocks]")
+    index = _device_index(q, k_cache, v_cache, k_scales, v_scales, block_table, seqlens_k, seqlens_q, out, lse,
+                          workspace, error_flags, cu_seqlens_q)
+    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    if code != ATTN_DTYPE_FP8_E4M3:
+        raise ValueError("E4M3 caches")
+    if q.shape[-1] != D:
+        raise ValueError("caches of q's head_dim")
+    B = seqlens_k.numel()
+    _table(block_table, B)
     _i32_vec(seqlens_k, B, "seqlens_k")
     if seqlens_q is not None:
         _i32_vec(seqlens_q, B, "seqlens_q")
     p = PrefillParams()
     out, lse = _queries(p, q, out, lse, out_dtype, want_lse, B, cu_seqlens_q, max_seqlen_q)
-    p.k_cache, p.v_cache, p.block_table = _ptr(k_cache), _ptr(v_cache), _ptr(block_table)
-    p.seqlens_k, p.seqlens_q = _ptr(seqlens_k), _ptr(seqlens_q)
+    p.k_cache, p.v_cache, p.block_table = k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
+    p.seqlens_k, p.seqlens_q = seqlens_k.data_ptr(), _opt(seqlens_q)
     p.batch, p.num_kv_heads = B, Hkv
-    p.seqlen_k = block_table.shape[1] * BS if max_seqlen_k is None else int(max_seqlen_k)
-    p.max_blocks_per_seq, p.num_blocks, p.block_size = block_table.shape[1], NB, BS
-    p.scale, p.causal = float(scale if scale is not None else 1.0 / math.sqrt(D)), int(bool(causal))
-    p.error_flags = _ptr(error_flags)
-    _call_with_workspace(LIB.attn_prefill_paged_block_scaled, "attn_prefill_paged_block_scaled", dev, p, k_scales,
+    p.seqlen_k = block_table.shape[1] * 16 if max_seqlen_k is None else int(max_seqlen_k)
+    p.max_blocks_per_seq, p.num_blocks, p.block_size = block_table.shape[1], NB, 16
+    p.scale, p.causal = 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0
+    p.error_flags = _opt(error_flags)
+    _call_with_workspace(LIB.attn_prefill_paged_block_scaled, "attn_prefill_paged_block_scaled", index, p, k_scales,
                          v_scales, workspace)
     return out, lse
 
