@@ -16,7 +16,7 @@ namespace rotary {
 constexpr int THREADS = 256;
 
 template <typename TI, typename TO, bool INTER>
-__global__ void __launch_bounds__(THREADS) rotary_kernel(const Rows r, const Turn t) {
+__global__ void __launch_bounds__(THREADS, 3) rotary_kernel(const Rows r, const Turn t) {
   turn_rows<TI, TO, INTER>(r, t, (long long)blockIdx.x * THREADS + threadIdx.x);
 }
 

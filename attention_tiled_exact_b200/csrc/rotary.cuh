@@ -58,19 +58,39 @@ __device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], cons
   }
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 r = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// Eight row elements as they lie in memory, and as fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* x) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
-}
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* x) {
+  Raw8<T> r;
+  r.load(p);
+  r.get(x);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -100,7 +120,9 @@ struct Rows {
 // Thread `index` of tokens * head_groups * units: unit index % units of one
 // token, for every head_groups-th head. Neighbouring lanes hold a row's units
 // (16-byte vectors, whole 128-byte lines for head_dim 128), then the next
-// token's. The rows of four heads are loaded before any is stored.
+// token's. The rows of several heads are on their way while the angles are
+// computed, and the next ones while these are turned; they stay packed until
+// they are used, which keeps the kernel at 64 registers and 32 warps per SM.
 template <typename TI, typename TO, bool INTER>
 __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, long long index) {
   const int u = (int)(index % r.units);
@@ -112,35 +134,48 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, long lon
   const int position = r.positions ? __ldg(r.positions + token) : (int)pos_in_seq;
   if (r.slots ? __ldg(r.slots + token) < 0 : position < 0) return;
   const bool turned = u * 16 < t.rotary_dim;
-  float c[8], s[8];
-  if (turned) unit_turn(t, position, u, c, s);
   const int2 off = unit_offsets<INTER>(u, t.rotary_dim);
   const TI* q = reinterpret_cast<const TI*>(r.q) + b * r.q_bs + pos_in_seq * r.q_rs;
   const TI* k = reinterpret_cast<const TI*>(r.k) + b * r.k_bs + pos_in_seq * r.k_rs;
   TO* qo = reinterpret_cast<TO*>(r.q_out) + b * r.qo_bs + pos_in_seq * r.qo_rs;
   TO* ko = reinterpret_cast<TO*>(r.k_out) + b * r.ko_bs + pos_in_seq * r.ko_rs;
-  constexpr int BATCH = 4;
-  for (int h0 = group; h0 < r.heads; h0 += BATCH * r.head_groups) {
-    float x[BATCH][16];
+  constexpr int BATCH = sizeof(TI) == 2 ? 2 : 1;
+  Raw8<TI> raw[2][BATCH][2];
+  auto fetch = [&](int h0, Raw8<TI> (&to)[BATCH][2]) {
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const int h = h0 + i * r.head_groups;
       if (h < r.heads) {
         const TI* src = h < r.hq ? q + h * r.q_hs : k + (h - r.hq) * r.k_hs;
-        load8(src + off.x, &x[i][0]);
-        load8(src + off.y, &x[i][8]);
+        to[i][0].load(src + off.x);
+        to[i][1].load(src + off.y);
       }
     }
+  };
+  fetch(group, raw[0]);
+  float c[8], s[8];
+  if (turned) unit_turn(t, position, u, c, s);
+  auto finish = [&](int h0, const Raw8<TI> (&from)[BATCH][2]) {
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const int h = h0 + i * r.head_groups;
       if (h < r.heads) {
-        if (turned) turn16<INTER>(x[i], c, s);
+        float x[16];
+        from[i][0].get(x);
+        from[i][1].get(x + 8);
+        if (turned) turn16<INTER>(x, c, s);
         TO* dst = h < r.hq ? qo + h * r.qo_hs : ko + (h - r.hq) * r.ko_hs;
-        store8(dst + off.x, &x[i][0]);
-        store8(dst + off.y, &x[i][8]);
+        store8(dst + off.x, x);
+        store8(dst + off.y, x + 8);
       }
     }
+  };
+  const int step = BATCH * r.head_groups;
+  for (int h0 = group; h0 < r.heads; h0 += 2 * step) {
+    fetch(h0 + step, raw[1]);
+    finish(h0, raw[0]);
+    fetch(h0 + 2 * step, raw[0]);
+    finish(h0 + step, raw[1]);
   }
 }
 
@@ -148,7 +183,7 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, long lon
 // alone do not fill the machine, and fewer as they do, so that the angles of a
 // token are computed once for several heads.
 inline int head_groups_for(long long tokens, int heads, int units, int sm_count) {
-  const long long want = 1024LL * sm_count;  // threads: half of what the SMs hold
+  const long long want = 2048LL * sm_count;  // threads: two rounds of 1024 per SM
   long long g = tokens > 0 ? (want + tokens * units - 1) / (tokens * units) : 1;
   const long long least = (heads + 15) / 16;  // at most 16 heads a thread
   if (g < least) g = least;

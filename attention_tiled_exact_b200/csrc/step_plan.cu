@@ -2,14 +2,15 @@
 // prefix sums of the new tokens and of the blocks they need, then one position
 // and slot for each token and one table entry for each new block.
 //
-// One launch of one thread-block cluster. Every CTA scans the requests itself
-// (a few integers per thread, from L2) instead of waiting for another's sums,
-// keeps a chunk of the prefix sums in shared memory, and fills its share of
-// the chunk's rows, each finding its request by binary search. The cluster's
-// barrier stands between the last read of the lengths and the writes of the
-// advanced state, which may be the same memory. The bytes are few (8 per token
-// out): what bounds it is the launch and the chain load - scan - search - load.
-#include <cooperative_groups.h>
+// Every CTA scans the requests itself (a few integers per thread, from L2)
+// instead of waiting for another's sums, keeps a chunk of the prefix sums in
+// shared memory, and fills its share of the chunk's rows four at a time: one
+// binary search for the first row's request, then a walk. A step of up to
+// SMALL rows is one CTA, which also advances the state. A larger one takes as
+// many CTAs as its rows fill, and a dependent launch of one CTA advances the
+// state after all of them, because the new state may lie over the old one.
+// The bytes are few (8 per token out): what bounds it is the launch and the
+// chain load - scan - search - load.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -19,12 +20,11 @@
 namespace attn {
 namespace plan {
 
-namespace cg = cooperative_groups;
-
 constexpr int THREADS = 512;
 constexpr int CHUNK = 2048;  // requests whose prefix sums are in shared memory at once
 constexpr int PER = CHUNK / THREADS;
 constexpr int BS = 16;
+constexpr int SMALL = 4 * THREADS;  // rows that one CTA fills in one round
 
 struct Args {
   const int32_t* seq_lens;
@@ -39,6 +39,7 @@ struct Args {
   int32_t* used_out;
   int32_t* flags;
   int batch, max_blocks, num_blocks, num_free, total_q;
+  int vec;  // positions and slots are 16-byte aligned
 };
 
 // Sums of (tokens, blocks) in front of this thread's requests, over the block.
@@ -65,36 +66,59 @@ __device__ __forceinline__ void scan_pair(long long& tok, long long& blk, long l
   __syncthreads();
 }
 
+// A request's lengths, bounded to its table row.
+__device__ __forceinline__ void lengths(const Args& a, int b, int& s, int& n, int& faults) {
+  const int cap = a.max_blocks * BS;
+  s = a.seq_lens[b];
+  n = a.new_lens[b];
+  if (s < 0 || s > cap) {
+    faults |= ATTN_FAULT_BAD_LENGTH;
+    s = s < 0 ? 0 : cap;
+  }
+  if (n < 0 || n > cap - s) {
+    faults |= ATTN_FAULT_BAD_LENGTH;
+    n = n < 0 ? 0 : cap - s;
+  }
+}
+
+__device__ __forceinline__ int blocks_of(int tokens) { return (tokens + BS - 1) / BS; }
+
+// Blocks in use before the step, bounded to the free list.
+__device__ __forceinline__ int used_before(const Args& a, int& faults) {
+  const int used = a.num_used[0];
+  if (used >= 0 && used <= a.num_free) return used;
+  faults |= ATTN_FAULT_NO_BLOCK;
+  return used < 0 ? 0 : a.num_free;
+}
+
+// By one CTA, when a.cu is complete and nobody reads the old state any more:
+// the lengths and the blocks in use, for the rows that the step has.
+__device__ __forceinline__ void advance_state(const Args& a, int used, long long (*sums)[2]) {
+  long long none = 0, taken = 0;
+  int ignored = 0;  // the fill has flagged them
+  for (int b = threadIdx.x; b < a.batch; b += THREADS) {
+    int s, n;
+    lengths(a, b, s, n, ignored);
+    const int end = s + a.cu[b + 1] - a.cu[b];
+    taken += blocks_of(end) - blocks_of(s);
+    a.seq_out[b] = end;
+  }
+  long long all, none_all;
+  scan_pair(none, taken, none_all, all, sums);
+  if (threadIdx.x == 0) a.used_out[0] = (int)min(used + all, (long long)a.num_free);
+}
+
+template <bool ADVANCE>
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   __shared__ int s_cu[CHUNK + 1];    // the chunk's first rows, clipped to total_q
   __shared__ int s_seq[CHUNK];       // cached tokens
   __shared__ int s_base[CHUNK];      // place of the request's first new block in the free list, clipped to num_free
   __shared__ long long s_sums[THREADS / 32][2];
-  __shared__ unsigned long long s_taken;  // blocks taken for the tokens that have a row
-  if (threadIdx.x == 0) s_taken = 0;  // the first scan's barriers stand before its first use
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-  const int cap = a.max_blocks * BS;
+  const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;
+  if constexpr (!ADVANCE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int faults = 0;
-  int used = a.num_used ? a.num_used[0] : 0;
-  if (used < 0 || used > a.num_free) {
-    faults |= ATTN_FAULT_NO_BLOCK;
-    used = used < 0 ? 0 : a.num_free;
-  }
+  const int used = used_before(a, faults);
   long long tok_before = 0, blk_before = 0;  // of the chunks so far
-  // A request's lengths, bounded to its table row.
-  auto lengths = [&](int b, int& s, int& n) {
-    s = a.seq_lens[b];
-    n = a.new_lens[b];
-    if (s < 0 || s > cap) {
-      faults |= ATTN_FAULT_BAD_LENGTH;
-      s = s < 0 ? 0 : cap;
-    }
-    if (n < 0 || n > cap - s) {
-      faults |= ATTN_FAULT_BAD_LENGTH;
-      n = n < 0 ? 0 : cap - s;
-    }
-  };
   for (int c0 = 0; c0 < a.batch; c0 += CHUNK) {
     const int count = min(CHUNK, a.batch - c0);
     int s[PER], n[PER];
@@ -103,9 +127,9 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
     for (int i = 0; i < PER; ++i) {
       const int j = threadIdx.x * PER + i;
       s[i] = n[i] = 0;
-      if (j < count) lengths(c0 + j, s[i], n[i]);
+      if (j < count) lengths(a, c0 + j, s[i], n[i], faults);
       tok += n[i];
-      blk += (s[i] + n[i] + BS - 1) / BS - (s[i] + BS - 1) / BS;
+      blk += blocks_of(s[i] + n[i]) - blocks_of(s[i]);
     }
     long long tok_all, blk_all;
     scan_pair(tok, blk, tok_all, blk_all, s_sums);
@@ -119,43 +143,61 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
         s_seq[j] = s[i];
         s_base[j] = (int)min(blk, (long long)a.num_free);
         if (rank == 0) a.cu[c0 + j] = s_cu[j];
-        if (rank == 0 && n[i] > 0 && tok < a.total_q) {
-          const int rows = (int)min((long long)n[i], a.total_q - tok);
-          const int need = (s[i] + rows + BS - 1) / BS - (s[i] + BS - 1) / BS;
-          if (need) atomicAdd(&s_taken, (unsigned long long)need);
-        }
       }
       tok += n[i];
-      blk += (s[i] + n[i] + BS - 1) / BS - (s[i] + BS - 1) / BS;
+      blk += blocks_of(s[i] + n[i]) - blocks_of(s[i]);
     }
     tok_before += tok_all;
     blk_before += blk_all;
     if (threadIdx.x == 0) s_cu[count] = (int)min(tok_before, (long long)a.total_q);
     __syncthreads();
-    const int end = s_cu[count];
-    for (int t = s_cu[0] + rank * THREADS + threadIdx.x; t < end; t += ranks * THREADS) {
-      int lo = 0, hi = count;  // the last request whose first row is <= t: it has row t
+    const int begin = s_cu[0], end = s_cu[count];
+    // Rows 4 i .. 4 i + 3, as far as they are the chunk's.
+    for (int i = begin / 4 + rank * THREADS + threadIdx.x; 4LL * i < end; i += ranks * THREADS) {
+      const int t0 = max(4 * i, begin), t1 = (int)min(4LL * i + 4, (long long)end);
+      int lo = 0, hi = count;  // the last request whose first row is <= t0: it has row t0
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= t) lo = mid; else hi = mid;
+        if (s_cu[mid] <= t0) lo = mid; else hi = mid;
       }
-      const int pos = s_seq[lo] + (t - s_cu[lo]);
-      const int col = pos / BS, had = (s_seq[lo] + BS - 1) / BS;
-      int32_t* entry = a.table + (long long)(c0 + lo) * a.max_blocks + col;
-      const int at = s_base[lo] + (col - had);  // both terms below 2^30
-      int id = -1;
-      if (col >= had && at >= a.num_free) {
-        faults |= ATTN_FAULT_NO_BLOCK;
-      } else {
-        id = col < had ? *entry : a.free_blocks[at];
-        if (id < 0 || id >= a.num_blocks) {
-          faults |= ATTN_FAULT_BAD_BLOCK;
+      int pos[4], slot[4];
+      int id = -1, known = -1;  // the block of column `known` of request lo
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = 4 * i + j;
+        if (t < t0 || t >= t1) continue;
+        while (t >= s_cu[lo + 1]) ++lo, known = -1;  // past requests without rows too
+        const int p = s_seq[lo] + (t - s_cu[lo]);
+        const int col = p / BS, had = blocks_of(s_seq[lo]);
+        if (col != known) {
+          known = col;
+          int32_t* entry = a.table + (long long)(c0 + lo) * a.max_blocks + col;
+          const int at = s_base[lo] + (col - had);  // both terms below 2^30
           id = -1;
+          if (col >= had && at >= a.num_free) {
+            faults |= ATTN_FAULT_NO_BLOCK;
+          } else {
+            id = col < had ? *entry : a.free_blocks[at];
+            if (id < 0 || id >= a.num_blocks) {
+              faults |= ATTN_FAULT_BAD_BLOCK;
+              id = -1;
+            }
+          }
+          if (col >= had && p % BS == 0) *entry = id;
+        }
+        pos[j] = p;
+        slot[j] = id < 0 ? -1 : id * BS + p % BS;
+      }
+      if (a.vec && t1 - t0 == 4) {
+        *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = 4 * i + j;
+          if (t >= t0 && t < t1) a.positions[t] = pos[j], a.slots[t] = slot[j];
         }
       }
-      if (col >= had && pos % BS == 0) *entry = id;
-      a.positions[t] = pos;
-      a.slots[t] = id < 0 ? -1 : id * BS + pos % BS;
     }
     __syncthreads();  // the chunk's sums are overwritten next
   }
@@ -165,39 +207,44 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
     a.slots[t] = -1;
   }
   if (tok_before > a.total_q) faults |= ATTN_FAULT_BAD_LENGTH;
-  cluster.sync();  // every CTA has read the lengths and num_used
-  if (rank == 0) {
-    const int end = (int)min(tok_before, (long long)a.total_q);
-    for (int b = threadIdx.x; b < a.batch; b += THREADS) {
-      int s, n;
-      lengths(b, s, n);
-      a.seq_out[b] = s + ((b + 1 < a.batch ? a.cu[b + 1] : end) - a.cu[b]);  // a.cu: this CTA's own writes
-    }
-    if (threadIdx.x == 0) {
-      a.cu[a.batch] = end;
-      a.used_out[0] = (int)min((long long)(used + s_taken), (long long)a.num_free);
-    }
-  }
   if (faults && a.flags) atomicOr(a.flags, faults);
+  if (rank == 0 && threadIdx.x == 0) a.cu[a.batch] = (int)min(tok_before, (long long)a.total_q);
+  if constexpr (ADVANCE) {
+    __syncthreads();
+    advance_state(a, used, s_sums);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS) advance_kernel(const Args a) {
+  __shared__ long long s_sums[THREADS / 32][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int ignored = 0;
+  advance_state(a, used_before(a, ignored), s_sums);
 }
 
 }  // namespace plan
 
 attn_status_t launch_plan(const attn_plan_params& p, cudaStream_t stream) {
+  const bool vec = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slot_map)) & 15u) == 0;
   const plan::Args a = {p.seq_lens, p.new_lens, p.block_table, p.free_blocks, p.num_used, p.seq_lens_out,
                         p.cu_seqlens_q, p.positions, p.slot_map, p.num_used_out, p.error_flags, p.batch,
-                        p.max_blocks_per_seq, p.num_blocks, p.num_free, p.total_q};
+                        p.max_blocks_per_seq, p.num_blocks, p.num_free, p.total_q, vec ? 1 : 0};
+  if (p.total_q <= plan::SMALL) {
+    plan::plan_kernel<true><<<1, plan::THREADS, 0, stream>>>(a);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
+  const int want = (p.total_q + plan::SMALL - 1) / plan::SMALL, sms = device_sm_count();
+  plan::plan_kernel<false><<<want < sms ? want : sms, plan::THREADS, 0, stream>>>(a);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.total_q > 4 * plan::THREADS ? 8 : 1;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(attr[0].val.clusterDim.x);
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(plan::THREADS);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, plan::plan_kernel, a) != cudaSuccess) {
+  if (cudaGetLastError() != cudaSuccess || cudaLaunchKernelEx(&cfg, plan::advance_kernel, a) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_CUDA;
   }
