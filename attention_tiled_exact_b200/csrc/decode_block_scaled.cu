@@ -11,13 +11,18 @@
 // a sequence's blocks lie apart. Both maxima are kept stale until they grow by
 // 2^8.
 //
-// One CTA of 4 warps handles one split of one (sequence, kv head); the query
-// heads of the group are the rows of a 16-row matrix product, so a block is
+// One CTA of 4 warps handles one split of one (sequence, kv head), so a block is
 // read from HBM once for the group. Each warp walks every 4th block: K and V
 // codes come through a per-warp ring of cp.async stages, are widened exactly to
-// fp16 (cvt.rn.f16x2.e4m3x2) and go to mma.sync m16n8k16 with fp32 sums. The
-// ring's 16-byte chunks are swizzled so that the K reads (a row per 4 lanes)
+// fp16 (cvt.rn.f16x2.e4m3x2) and go to mma.sync m16n8k16 with fp32 sums. Both
+// products are computed transposed, S' = K q' and O' = V' P', with the tokens or
+// the elements as the 16 rows and the group's heads as the 8 columns: half the
+// products of the other order, which would pad a group of 8 to 16 rows. P'
+// changes its lane layout between the two with movmatrix.
+// The ring's 16-byte chunks are swizzled so that the K reads (a row per 4 lanes)
 // and the V reads (a column slice per 8 lanes) are free of bank conflicts.
+// The running maxima move only when some lane's score exceeds them by 2^8: one
+// vote per block stands in for the shuffles of a maximum over its tokens.
 // Queries enter in fp16 too: each row is first scaled by a power of two that
 // brings its largest element into [2^14, 2^15), and the scores are scaled back,
 // so that no bf16 query overflows (elements 2^29 below the row's largest one
@@ -39,7 +44,7 @@ namespace bsdecode {
 constexpr int BS = 16;
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int STAGES = 4;
+constexpr int STAGES = 3;
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -95,12 +100,18 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The 8 x 8 matrix of 16-bit elements whose row lane / 4 holds the lane's two, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Four codes as two fp16 pairs (elements 0, 1 and 2, 3).
@@ -135,11 +146,11 @@ __device__ __forceinline__ T* o_row(const Args& a, int b, int head, int d) {
   return reinterpret_cast<T*>(a.o) + ((long long)b * a.hq + head) * d;
 }
 
-// HALVES: 8-row halves of the products' 16 rows that hold query heads (group <= 8 * HALVES).
+// HALVES: groups of 8 columns that hold query heads (group <= 8 * HALVES).
 template <int D, int HALVES>
-__global__ void __launch_bounds__(THREADS) split_kernel(const Args a) {
+__global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(const Args a) {
   constexpr int ROWS = 8 * HALVES;
-  constexpr int KSTEPS = D / 16, NT = D / 8;
+  constexpr int KSTEPS = D / 16, MT = D / 16;
   constexpr int COPIES = BS * D / (16 * 32);  // 16-byte copies per lane and block
   extern __shared__ __align__(128) uint8_t smem[];
   Ring<D>& ring = *reinterpret_cast<Ring<D>*>(smem);
@@ -204,10 +215,10 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const Args a) {
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s);
 
-  // A fragments of q: head gq (and gq + 8), elements (D / 4) tq + 4 step + 0..3,
-  // the order in which the lane reads its K row slice.
-  uint32_t qa[KSTEPS][2 * HALVES];
-  float row_scale[HALVES];  // score of the scaled query -> log2 units
+  // B fragments of q: head gq (and gq + 8), elements (D / 4) tq + 4 step + 0..3,
+  // the order in which the lane reads its K row slices.
+  uint32_t qb[HALVES][KSTEPS][2];
+  float mul[HALVES][2];  // score of the scaled query of heads 2 tq, 2 tq + 1 (+ 8 h) -> log2 units
 #pragma unroll
   for (int h = 0; h < HALVES; ++h) {
     const int g = gq + 8 * h;
@@ -228,25 +239,30 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const Args a) {
     // 2^e scales the row; bounded so that 2^e and 2^-e are normal fp32 numbers.
     const int e = min(max(14 - ((int)(__float_as_uint(top) >> 23) - 127), -113), 113);
     const float up = top > 0.f ? bscale::pow2i(e) : 1.f;
-    row_scale[h] = a.scale_log2 * (top > 0.f ? bscale::pow2i(-e) : 1.f);
+    const float back = a.scale_log2 * (top > 0.f ? bscale::pow2i(-e) : 1.f);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) mul[h][j] = __shfl_sync(FULL, back, 4 * (2 * tq + j));
 #pragma unroll
     for (int ks = 0; ks < KSTEPS; ++ks)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t x = w[2 * ks + j];
-        qa[ks][HALVES * j + h] = pack_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
+        qb[h][ks][j] = pack_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
       }
   }
 
-  // O of head gq (+ 8 h), element (D / 4) tq + (D / 8) j + nt, in ot[nt][2 h + j], in units of 2^r.
-  float ot[NT][2 * HALVES];
+  // O of element (D / 8) gq + 2 mt + i / 2, head 2 tq + i % 2 (+ 8 h) in ot[h][mt][i], in units of 2^r.
+  float ot[HALVES][MT][4];
+  float m[HALVES][2], r[HALVES][2], l[HALVES][2];  // l: this lane's tokens only, until the end
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
-    for (int j = 0; j < 2 * HALVES; ++j) ot[nt][j] = 0.f;
-  float m[HALVES], r[HALVES], l[HALVES];  // l: this lane's tokens only, until the end
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-  for (int h = 0; h < HALVES; ++h) m[h] = r[h] = -INFINITY, l[h] = 0.f;
+      for (int i = 0; i < 4; ++i) ot[h][mt][i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) m[h][j] = r[h][j] = -INFINITY, l[h][j] = 0.f;
+  }
 
   for (int n = 0; n < n_mine; ++n) {
     issue(n + STAGES - 1);
@@ -260,78 +276,97 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const Args a) {
     if (n_valid > 0) {
       const uint8_t* kblk = ring.kv[warp][n % STAGES][0];
       const uint8_t* vblk = ring.kv[warp][n % STAGES][1];
-      float c[2][4];
+      // ---- S' = K q': tokens gq (x[h][0], x[h][1]: heads 2 tq, 2 tq + 1) and gq + 8 (x[h][2], x[h][3])
+      float x[HALVES][4];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        uint32_t kw[D / 16];
+      for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          const uint4 x = *reinterpret_cast<const uint4*>(kblk + swz<D>(8 * nt + gq, (D / 64) * tq + i));
-          kw[4 * i] = x.x, kw[4 * i + 1] = x.y, kw[4 * i + 2] = x.z, kw[4 * i + 3] = x.w;
-        }
+        for (int i = 0; i < 4; ++i) x[h][i] = 0.f;
+      {
+        uint32_t kw[2][D / 16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c[nt][j] = 0.f;
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(kblk + swz<D>(8 * nt + gq, (D / 64) * tq + i));
+            kw[nt][4 * i] = w.x, kw[nt][4 * i + 1] = w.y, kw[nt][4 * i + 2] = w.z, kw[nt][4 * i + 3] = w.w;
+          }
 #pragma unroll
         for (int ks = 0; ks < KSTEPS; ++ks) {
-          uint32_t b0, b1;
-          widen4(kw[ks], b0, b1);
-          if constexpr (HALVES == 2)
-            mma_f16(c[nt], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
-          else
-            mma_f16(c[nt], qa[ks][0], 0u, qa[ks][1], 0u, b0, b1);
+          uint32_t ka[4];
+          widen4(kw[0][ks], ka[0], ka[2]);
+          widen4(kw[1][ks], ka[1], ka[3]);
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) mma_f16(x[h], ka, qb[h][ks][0], qb[h][ks][1]);
         }
       }
       // ---- the two running maxima and the weights
       const float k_mul = bscale::scale_of(sc & 0xff);
       const int vb = sc >> 8;
       const float ev = vb == 255 ? NAN : (float)(vb - bscale::BIAS);
-      uint32_t pa[2][HALVES];
+      bool over = false;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float f = mul[h][j] * k_mul;
+          x[h][j] = gq < n_valid ? x[h][j] * f : -INFINITY;
+          x[h][2 + j] = gq + 8 < n_valid ? x[h][2 + j] * f : -INFINITY;
+          const float top = fmaxf(x[h][j], x[h][2 + j]);
+          over |= top - m[h][j] > RESCALE_THRESHOLD || top + ev - r[h][j] > RESCALE_THRESHOLD;
+        }
+      if (__any_sync(FULL, over)) {
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(x[h][j], x[h][2 + j]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+            const float m_new = fmaxf(m[h][j], top), r_new = fmaxf(r[h][j], top + ev);
+            if (m_new > m[h][j]) {
+              l[h][j] *= ex2_approx(m[h][j] - m_new);
+              m[h][j] = m_new;
+            }
+            if (r_new > r[h][j]) {
+              const float alpha = ex2_approx(r[h][j] - r_new);
+              r[h][j] = r_new;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) ot[h][mt][j] *= alpha, ot[h][mt][2 + j] *= alpha;
+            }
+          }
+      }
+      uint32_t pb[HALVES][2];
 #pragma unroll
       for (int h = 0; h < HALVES; ++h) {
-        const float mul = row_scale[h] * k_mul;
-        float x[4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            x[2 * nt + j] = 8 * nt + 2 * tq + j < n_valid ? c[nt][2 * h + j] * mul : -INFINITY;
-        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-        top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-        const float m_new = fmaxf(m[h], top), r_new = fmaxf(r[h], top + ev);
-        if (m_new - m[h] > RESCALE_THRESHOLD) {
-          l[h] *= ex2_approx(m[h] - m_new);
-          m[h] = m_new;
-        }
-        if (r_new - r[h] > RESCALE_THRESHOLD) {
-          const float alpha = ex2_approx(r[h] - r_new);
-          r[h] = r_new;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) ot[nt][2 * h] *= alpha, ot[nt][2 * h + 1] *= alpha;
-        }
-        const float ms = m[h] == -INFINITY ? 0.f : m[h];
-        // 2^(ev + m - r): the softmax's weight to O's. Bounded, so that a weight of 0 stays 0.
-        float f = r[h] == -INFINITY ? ev : ev + ms - r[h];
-        f = ex2_approx(f > 126.f ? 126.f : f);
         float p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = ex2_approx(x[j] - ms);
-        l[h] += (p[0] + p[1]) + (p[2] + p[3]);
-        // fp16 weights: half a step is 2^-12 of the weight, below the rounding of a bf16 result.
-        pa[0][h] = pack_f16x2(p[0] * f, p[1] * f);
-        pa[1][h] = pack_f16x2(p[2] * f, p[3] * f);
+        for (int j = 0; j < 2; ++j) {
+          const float ms = m[h][j] == -INFINITY ? 0.f : m[h][j];
+          // 2^(ev + m - r): the softmax's weight to O's. Bounded, so that a weight of 0 stays 0.
+          float f = r[h][j] == -INFINITY ? ev : ev + ms - r[h][j];
+          f = ex2_approx(f > 126.f ? 126.f : f);
+          p[j] = ex2_approx(x[h][j] - ms);
+          p[2 + j] = ex2_approx(x[h][2 + j] - ms);
+          l[h][j] += p[j] + p[2 + j];
+          p[j] *= f;
+          p[2 + j] *= f;
+        }
+        // fp16 weights: half a step is 2^-11 of the weight, below the rounding of a bf16 result.
+        pb[h][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+        pb[h][1] = transpose8x8(pack_f16x2(p[2], p[3]));
       }
-      // ---- O += P V on the codes: rows 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, elements (D / 8) gq + nt
+      // ---- O' += V' P' on the codes: tokens 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9, elements (D / 8) gq + ..
       uint32_t vr[4][D / 32];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tk = 2 * tq + (i & 1) + 8 * (i >> 1);
         if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vblk + swz<D>(tk, gq));
-          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][2] = x.z, vr[i][3] = x.w;
+          const uint4 w = *reinterpret_cast<const uint4*>(vblk + swz<D>(tk, gq));
+          vr[i][0] = w.x, vr[i][1] = w.y, vr[i][2] = w.z, vr[i][3] = w.w;
         } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vblk + swz<D>(tk, gq >> 1) + 8 * (gq & 1));
-          vr[i][0] = x.x, vr[i][1] = x.y;
+          const uint2 w = *reinterpret_cast<const uint2*>(vblk + swz<D>(tk, gq >> 1) + 8 * (gq & 1));
+          vr[i][0] = w.x, vr[i][1] = w.y;
         }
       }
       if (n_valid < BS) {  // a weight of 0 must not meet what lies behind the last token
@@ -345,47 +380,34 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const Args a) {
       for (int w = 0; w < D / 32; ++w)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const uint32_t sel = half ? 0x7362u : 0x5140u;  // bytes 2, 3 or 0, 1 of both rows, interleaved
-          uint32_t b0[2], b1[2];
-          widen4(__byte_perm(vr[0][w], vr[1][w], sel), b0[0], b0[1]);
-          widen4(__byte_perm(vr[2][w], vr[3][w], sel), b1[0], b1[1]);
+          const uint32_t sel = half ? 0x7362u : 0x5140u;  // bytes 2, 3 or 0, 1 of both tokens, interleaved
+          uint32_t va[4];
+          widen4(__byte_perm(vr[0][w], vr[1][w], sel), va[0], va[1]);
+          widen4(__byte_perm(vr[2][w], vr[3][w], sel), va[2], va[3]);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int nt = 4 * w + 2 * half + i;
-            float acc[4] = {ot[nt][0], ot[nt][1], 0.f, 0.f};
-            if constexpr (HALVES == 2) {
-              acc[2] = ot[nt][2], acc[3] = ot[nt][3];
-              mma_f16(acc, pa[0][0], pa[0][1], pa[1][0], pa[1][1], b0[i], b1[i]);
-              ot[nt][2] = acc[2], ot[nt][3] = acc[3];
-            } else {
-              mma_f16(acc, pa[0][0], 0u, pa[1][0], 0u, b0[i], b1[i]);
-            }
-            ot[nt][0] = acc[0], ot[nt][1] = acc[1];
-          }
+          for (int h = 0; h < HALVES; ++h) mma_f16(ot[h][2 * w + half], va, pb[h][0], pb[h][1]);
         }
     }
     __syncwarp();  // the slot is refilled by the next issue
   }
   cp_async_wait<0>();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- merge the warps
   __syncthreads();  // the ring becomes the merge buffer
   Merge<D, ROWS>& mg = *reinterpret_cast<Merge<D, ROWS>*>(smem);
 #pragma unroll
-  for (int h = 0; h < HALVES; ++h) {
-    l[h] += __shfl_xor_sync(FULL, l[h], 1);
-    l[h] += __shfl_xor_sync(FULL, l[h], 2);
-    const int g = gq + 8 * h;
-    if (tq == 0) mg.m[warp][g] = m[h], mg.r[warp][g] = r[h], mg.l[warp][g] = l[h];
-    float* dst = &mg.o[warp][g][(D / 4) * tq];
+  for (int h = 0; h < HALVES; ++h)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j) {
 #pragma unroll
-      for (int i = 0; i < NT / 4; ++i)
-        *reinterpret_cast<float4*>(dst + (D / 8) * j + 4 * i) =
-            make_float4(ot[4 * i][2 * h + j], ot[4 * i + 1][2 * h + j], ot[4 * i + 2][2 * h + j],
-                        ot[4 * i + 3][2 * h + j]);
-  }
+      for (int d = 4; d < 32; d <<= 1) l[h][j] += __shfl_xor_sync(FULL, l[h][j], d);
+      const int g = 8 * h + 2 * tq + j;
+      if (gq == 0) mg.m[warp][g] = m[h][j], mg.r[warp][g] = r[h][j], mg.l[warp][g] = l[h][j];
+      float2* dst = reinterpret_cast<float2*>(&mg.o[warp][g][(D / 8) * gq]);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) dst[mt] = make_float2(ot[h][mt][j], ot[h][mt][2 + j]);
+    }
   __syncthreads();
   const long long rows = (long long)a.batch * a.hq;
   for (int i = threadIdx.x; i < a.group * D; i += THREADS) {
@@ -420,30 +442,66 @@ __global__ void __launch_bounds__(THREADS) split_kernel(const Args a) {
   }
 }
 
-// One block per row of more than one split: O = sum_s e^(lse_s - lse) O_s.
+// One block per row of more than one split: O = sum_s e^(lse_s - lse) O_s, the
+// splits dealt out to 4 warps. A dependent launch: it is set up while the last
+// splits run.
 template <int D>
-__global__ void __launch_bounds__(D) combine_kernel(const Args a, int max_splits) {
-  const int row = blockIdx.x, b = row / a.hq;
+__global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int max_splits) {
+  constexpr int PER = D / 32;
+  __shared__ float s_m[WARPS], s_sum[WARPS], s_acc[WARPS][D];
+  const int row = blockIdx.x, b = row / a.hq, warp = warp_id(), lane = lane_id();
   const int T = a.split_tokens, L = bounded_len(a, b, max_splits, false);
   const int n = (L + T - 1) / T;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (n <= 1) return;
   const long long rows = (long long)a.batch * a.hq;
   const float* lse = a.part_lse + row;
   float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, lse[s * rows]);
+  for (int s = threadIdx.x; s < n; s += THREADS) M = fmaxf(M, __ldcg(lse + s * rows));
+#pragma unroll
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, d));
+  if (lane == 0) s_m[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
   const float Ms = M == -INFINITY ? 0.f : M;
-  float sum = 0.f, acc = 0.f;
-  for (int s = 0; s < n; ++s) {
-    const float w = ex2_approx((lse[s * rows] - Ms) * LOG2E);
+  float sum = 0.f, acc[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int s = warp; s < n; s += WARPS) {
+    const float w = ex2_approx((__ldcg(lse + s * rows) - Ms) * LOG2E);
+    const float* src = a.part_o + (s * rows + row) * D + lane * PER;
+    float x[PER];
+    if constexpr (PER == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      x[0] = v.x, x[1] = v.y;
+    }
     sum += w;
-    acc = fmaf(w, a.part_o[(s * rows + row) * D + threadIdx.x], acc);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, x[i], acc[i]);
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) sum += s_sum[w];
   const bool empty = sum == 0.f;
-  const float out = empty ? 0.f : acc / sum;
-  if (a.o_f32)
-    reinterpret_cast<float*>(a.o)[(long long)row * D + threadIdx.x] = out;
-  else
-    reinterpret_cast<__nv_bfloat16*>(a.o)[(long long)row * D + threadIdx.x] = __float2bfloat16_rn(out);
+  if (threadIdx.x < D) {
+    float out = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) out += s_acc[w][threadIdx.x];
+    out = empty ? 0.f : out / sum;
+    if (a.o_f32)
+      reinterpret_cast<float*>(a.o)[(long long)row * D + threadIdx.x] = out;
+    else
+      reinterpret_cast<__nv_bfloat16*>(a.o)[(long long)row * D + threadIdx.x] = __float2bfloat16_rn(out);
+  }
   if (threadIdx.x == 0 && a.lse) a.lse[row] = empty ? -INFINITY : Ms + log2f(sum) * LN2;
 }
 
@@ -461,8 +519,22 @@ static attn_status_t launch(const Args& a, int max_splits, cudaStream_t stream) 
   });
   if (st != ATTN_OK) return st;
   kern<<<dim3(max_splits, a.hkv, a.batch), THREADS, SMEM, stream>>>(a);
-  if (max_splits > 1) combine_kernel<D><<<a.batch * a.hq, D, 0, stream>>>(a, max_splits);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  if (max_splits <= 1) return ATTN_OK;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.batch * a.hq);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, a, max_splits) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  return ATTN_OK;
 }
 
 }  // namespace bsdecode
