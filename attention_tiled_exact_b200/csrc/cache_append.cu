@@ -22,6 +22,8 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "block_scaled.cuh"
 #include "internal.h"
 #include "rotary.cuh"
@@ -177,58 +179,65 @@ struct Gather {
   int flag_width;  // a sequence over width is a fault
 };
 
-// One warp per (sequence, block, kv head): 16 rows of K and of V. A lane moves
-// 8 elements per step.
+// One warp per (sequence, block, kv head): 16 rows of K and of V. A lane
+// holds 8-element vectors of both pages, all on their way before the first is
+// stored, so that a warp's store covers 512 bytes in a row.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(THREADS) gather_kernel(const Gather g, long long items) {
+  // A dependent launch may set itself up; it waits for the whole of this one.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long item = (long long)blockIdx.x * WARPS + warp_id();
   if (item >= items) return;
   const int lane = lane_id();
   const int h = (int)(item % g.hkv);
   const int blk = (int)(item / g.hkv % g.blocks);
   const long long b = item / g.hkv / g.blocks;
+  const int row0 = blk * BS;
   int len = __ldg(g.seq_lens + b);
+  int id = blk < g.max_blocks ? __ldg(g.table + b * g.max_blocks + blk) : -1;
   if (lane == 0 && h == 0 && blk == 0 && g.flags &&
       (len < 0 || len > (long long)g.max_blocks * BS || (g.flag_width && len > g.width)))
     atomicOr(g.flags, ATTN_FAULT_BAD_LENGTH);
   len = min(min(max(len, 0), g.max_blocks * BS), g.width);
   const int end = g.zero_to ? min(g.width, (len + g.zero_to - 1) / g.zero_to * g.zero_to) : g.width;
-  const int row0 = blk * BS;
   if (row0 >= end) return;
-  int id = -1;
-  if (row0 < len) {
-    id = __ldg(g.table + b * g.max_blocks + blk);
-    if (id < 0 || id >= g.num_blocks) {
-      if (lane == 0 && g.flags) atomicOr(g.flags, ATTN_FAULT_BAD_BLOCK);
-      id = -1;
-    }
+  if (row0 < len && (id < 0 || id >= g.num_blocks)) {
+    if (lane == 0 && g.flags) atomicOr(g.flags, ATTN_FAULT_BAD_BLOCK);
+    id = -1;
   }
-  const int live = id >= 0 ? min(BS, len - row0) : 0, rows = min(BS, end - row0);
-  const long long page = ((long long)id * g.hkv + h) * (BS * D);  // elements
-  const long long out = ((b * g.hkv + h) * g.width + row0) * D;
+  const int live = row0 < len && id >= 0 ? min(BS, len - row0) : 0, rows = min(BS, end - row0);
+  using Raw = typename std::conditional<FP8, uint2, uint4>::type;
   constexpr int VECS = D / 8, STEPS = BS * VECS / 32;
+  const long long at = (long long)id * g.hkv + h;
+  Raw raw[2][STEPS];
+  float scale[2];
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    const uint8_t* pool = which ? g.v_cache : g.k_cache;
-    __nv_bfloat16* dst = (which ? g.v_out : g.k_out) + out;
-    float scale = 0.f;
-    if (FP8 && live > 0) scale = bscale::scale_of(__ldg((which ? g.v_scales : g.k_scales) + (long long)id * g.hkv + h));
+    const Raw* page = reinterpret_cast<const Raw*>(which ? g.v_cache : g.k_cache) + at * (BS * VECS);
+    scale[which] = FP8 && live > 0 ? bscale::scale_of(__ldg((which ? g.v_scales : g.k_scales) + at)) : 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-      const int v = i * 32 + lane, r = v / VECS;
-      if (r >= rows) continue;
-      if constexpr (FP8) {
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < live) {
-          bscale::load_codes8(pool + page + v * 8, x);
+      raw[which][i] = Raw{};
+      if ((i * 32 + lane) / VECS < live) raw[which][i] = __ldg(page + i * 32 + lane);
+    }
+  }
+  const long long out = ((b * g.hkv + h) * g.width + row0) * D;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] *= scale;
-        }
-        rotary::store8(dst + v * 8, x);
+  for (int which = 0; which < 2; ++which) {
+    uint4* dst = reinterpret_cast<uint4*>((which ? g.v_out : g.k_out) + out);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const int v = i * 32 + lane;
+      if (v / VECS >= rows) continue;
+      if constexpr (FP8) {
+        const uint2 r = raw[which][i];
+        const float mul = v / VECS < live ? scale[which] : 0.f;
+        const float2 x0 = bscale::codes_to_float2(r.x & 0xffffu), x1 = bscale::codes_to_float2(r.x >> 16);
+        const float2 x2 = bscale::codes_to_float2(r.y & 0xffffu), x3 = bscale::codes_to_float2(r.y >> 16);
+        dst[v] = make_uint4(pack_bf16x2(x0.x * mul, x0.y * mul), pack_bf16x2(x1.x * mul, x1.y * mul),
+                            pack_bf16x2(x2.x * mul, x2.y * mul), pack_bf16x2(x3.x * mul, x3.y * mul));
       } else {
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (r < live) x = *reinterpret_cast<const uint4*>(pool + (page + v * 8) * 2);
-        *reinterpret_cast<uint4*>(dst + v * 8) = x;
+        dst[v] = raw[which][i];
       }
     }
   }

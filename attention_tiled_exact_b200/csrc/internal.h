@@ -63,6 +63,13 @@ attn_status_t validate_decode(const attn_decode_params* p);
 // Prefill launcher. Arguments were validated by the caller.
 attn_status_t launch_prefill(const attn_prefill_params& p, cudaStream_t stream);
 
+// The same for dense keys and values that the launch just before on the stream
+// writes (a kernel that lets dependent launches start early). The key blocks of
+// an item may be shared by several CTAs; their partial results go to the
+// workspace (prefill_split_workspace_bytes of the same parameters, 16-byte aligned).
+attn_status_t launch_prefill_behind(const attn_prefill_params& p, void* split_workspace, cudaStream_t stream);
+size_t prefill_split_workspace_bytes(const attn_prefill_params& p);
+
 // Non-blocking streams of the current device (which = 0 or 1), created once
 // and kept for the process: the extra streams of calls that overlap kernels
 // or copies with their main stream.

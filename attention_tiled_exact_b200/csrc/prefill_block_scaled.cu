@@ -22,7 +22,25 @@ static size_t dense_bytes(const attn_prefill_params& p) {
   return (n + 255) / 256 * 256;
 }
 
-size_t prefill_block_scaled_workspace_bytes(const attn_prefill_params& p) { return 2 * dense_bytes(p); }
+// The call over the dense copy at `k`, V behind K.
+static attn_prefill_params dense_params(const attn_prefill_params& p, uint8_t* k) {
+  const int width = dense_width(p);
+  attn_prefill_params d = p;
+  d.k_cache = d.v_cache = nullptr;
+  d.block_table = nullptr;
+  d.max_blocks_per_seq = d.num_blocks = d.block_size = 0;
+  d.k = width > 0 ? k : nullptr;
+  d.v = width > 0 ? k + dense_bytes(p) : nullptr;
+  d.seqlen_k = width;
+  d.k_row_stride = d.v_row_stride = p.head_dim;
+  d.k_head_stride = d.v_head_stride = (int64_t)width * p.head_dim;
+  d.k_batch_stride = d.v_batch_stride = (int64_t)p.num_kv_heads * width * p.head_dim;
+  return d;
+}
+
+size_t prefill_block_scaled_workspace_bytes(const attn_prefill_params& p) {
+  return 2 * dense_bytes(p) + prefill_split_workspace_bytes(dense_params(p, nullptr));
+}
 
 attn_status_t launch_prefill_block_scaled(const attn_prefill_params& p, const uint8_t* k_scales,
                                           const uint8_t* v_scales, void* workspace, cudaStream_t stream) {
@@ -36,17 +54,7 @@ attn_status_t launch_prefill_block_scaled(const attn_prefill_params& p, const ui
   // last tile is cleared, nothing behind it is touched.
   const attn_status_t st = launch_gather(g, 128, true, stream);
   if (st != ATTN_OK) return st;
-  attn_prefill_params d = p;
-  d.k_cache = d.v_cache = nullptr;
-  d.block_table = nullptr;
-  d.max_blocks_per_seq = d.num_blocks = d.block_size = 0;
-  d.k = width > 0 ? k : nullptr;
-  d.v = width > 0 ? v : nullptr;
-  d.seqlen_k = width;
-  d.k_row_stride = d.v_row_stride = p.head_dim;
-  d.k_head_stride = d.v_head_stride = (int64_t)width * p.head_dim;
-  d.k_batch_stride = d.v_batch_stride = (int64_t)p.num_kv_heads * width * p.head_dim;
-  return launch_prefill(d, stream);
+  return launch_prefill_behind(dense_params(p, k), v + dense_bytes(p), stream);
 }
 
 }  // namespace attn

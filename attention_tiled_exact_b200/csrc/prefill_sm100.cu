@@ -117,6 +117,10 @@ struct Args {
   long long wait_limit;  // cycle bound of every pipeline wait
   int planted;           // debug build: bounds-check site reported as failed
   long long out_rows;    // rows per (batch, head) of O: seqlen_q, or total_q when packed
+  // partial results of items that several CTAs share (SPLIT kernels only)
+  float* part_o;    // [CTA][2][tile][D / 4][BM][4], normalised: a warp's rows side by side
+  float* part_lse;  // [CTA][2][tile][BM], natural log
+  int4* shares;     // [CTA]: see split_items
   // paged keys/values (PAGED kernels only)
   const int32_t* block_table;
   int max_blocks;
@@ -153,11 +157,35 @@ struct Work {
   int active[2];
   int n_kv[2];  // key blocks of BK each
   int sq, sk;
+  int lo;     // SPLIT: first key block of this piece (n_kv then counts the piece's blocks)
+  bool part;  // SPLIT: the piece is not the whole item
 };
 
+template <bool SPLIT = false>
 __device__ __forceinline__ Work decode_work(const Args& a, int item) {
   Work w;
-  if (a.pair_heads) {
+  if (SPLIT && a.pair_heads) {
+    // fd_outer: row blocks * pairs, fd_mid: pairs, fd_inner: hkv. Neighbouring
+    // items share their keys.
+    const int q0 = a.fd_outer.div(item);
+    const int r = item - q0 * a.fd_outer.d;
+    const int q1 = a.fd_mid.div(r);
+    w.b = a.fd_inner.div(q0);
+    w.kvh = q0 - w.b * a.hkv;
+    w.head[0] = w.kvh * a.group + 2 * (r - q1 * a.fd_mid.d);
+    w.head[1] = w.head[0] + 1;
+    w.row0[0] = w.row0[1] = (a.n_row_blocks - 1 - q1) * BM;
+  } else if (SPLIT) {
+    // fd_outer: row-block pairs, fd_mid: hq, fd_inner: group
+    const int q0 = a.fd_outer.div(item);
+    const int p = a.fd_outer.d - 1 - (item - q0 * a.fd_outer.d);
+    w.b = a.fd_mid.div(q0);
+    const int h = q0 - w.b * a.hq;
+    w.kvh = a.fd_inner.div(h);
+    w.head[0] = w.head[1] = h;
+    w.row0[0] = 2 * p * BM;
+    w.row0[1] = (2 * p + 1) * BM;
+  } else if (a.pair_heads) {
     // fd_outer: batch * hkv * pairs, fd_mid: pairs, fd_inner: hkv
     const int pairs = a.fd_mid.d;
     const int q0 = a.fd_outer.div(item);
@@ -212,6 +240,8 @@ __device__ __forceinline__ Work decode_work(const Args& a, int item) {
     }
     w.n_kv[t] = w.active[t] ? (kend + BK - 1) / BK : 0;
   }
+  w.lo = 0;
+  w.part = false;
   return w;
 }
 
@@ -269,9 +299,100 @@ __device__ void order_items(const Args& a, int n_items, unsigned long long* keys
   __syncthreads();
 }
 
+// SPLIT: the items' key blocks are dealt out evenly, cut where a CTA's share
+// ends, so that a few long items (or one) fill the machine as well as many.
+// An item costs its key blocks plus a fixed 11/8 of a block (as in
+// order_items); CTA c takes the c-th of gridDim.x equal parts of the items' total in
+// item order. Every CTA computes all costs (scratch: the K ring) and finds its
+// two boundaries, each an item and the first block behind it: share[] = first
+// item and block, last item and block (excluded), number of items touched.
+// An item that is cut leaves partial results, at most two per CTA: one of the
+// item that a CTA before it began (shares[c].x) and
+// one of an item that it begins itself (shares[c].z); -1 stands for none. The
+// CTAs of one item follow one another: inside an item a share is at least a
+// block, because it is MIN_SHARE of cost at least.
+constexpr int SPLIT_MIN_KEYS = 4 * BK;  // up to this bound of the keys an item is not worth cutting
+constexpr int MIN_SHARE = 16;  // eighths of a block: a CTA without 2 blocks' worth gets none
+template <int NT>
+__device__ void split_items(const Args& a, int n_items, int* cost, int* share) {
+  long long* sums = reinterpret_cast<long long*>(cost + SORT_MAX_ITEMS);
+  const int per = (n_items + NT - 1) / NT;
+  const int i0 = min(n_items, (int)threadIdx.x * per), i1 = min(n_items, i0 + per);
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) {
+    const Work w = decode_work<true>(a, i);
+    cost[i] = (w.active[0] || w.active[1]) ? max(w.n_kv[0], w.n_kv[1]) * 8 + 11 : 0;
+    mine += cost[i];
+  }
+  long long before = mine;  // inclusive sum over the warp, then exclusive over the block
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane_id() >= d) before += x;
+  }
+  if (lane_id() == 31) sums[warp_id()] = before;
+  if (threadIdx.x == 0) {
+    share[0] = share[2] = n_items;
+    share[1] = share[3] = 0;
+  }
+  __syncthreads();
+  long long total = 0;
+  before -= mine;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp_id()) before += sums[w];
+    total += sums[w];
+  }
+  const long long parts = max(1ll, min((long long)gridDim.x, total / MIN_SHARE));
+  for (int e = 0; e < 2; ++e) {
+    const long long c = (long long)blockIdx.x + e;
+    if (c > parts) continue;
+    // total < 2^31 items * 2^31: split the product so that it stays in 64 bits.
+    const long long x = total / parts * c + total % parts * c / parts;
+    long long p = before;
+    for (int i = i0; i < i1; p += cost[i], ++i) {
+      if (x < p || x >= p + cost[i]) continue;
+      const int off = (int)(x - p), n = (cost[i] - 11) / 8;
+      const int blk = off <= 8 ? 0 : min(n, (off - 4) / 8);
+      share[2 * e] = blk > 0 && blk == n ? i + 1 : i;
+      share[2 * e + 1] = blk == n ? 0 : blk;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const bool none = (long long)blockIdx.x >= parts || (share[0] == share[2] && share[1] == share[3]);
+    const bool one = share[0] == share[2];
+    share[4] = none ? 0 : share[2] - share[0] + (share[3] > 0 ? 1 : 0);
+    a.shares[blockIdx.x] = make_int4(!none && share[1] > 0 ? share[0] : -1, 0,
+                                     !none && share[3] > 0 && !(one && share[1] > 0) ? share[2] : -1, 0);
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+}
+
+// The piece of item w that lies in the CTA's share.
+__device__ __forceinline__ void clip_work(Work& w, int item, const int* share) {
+  const int n = max(w.n_kv[0], w.n_kv[1]);
+  w.lo = item == share[0] ? share[1] : 0;
+  const int hi = item == share[2] ? share[3] : n;
+  w.part = w.lo > 0 || hi < n;
+  for (int t = 0; t < 2; ++t) w.n_kv[t] = max(0, min(hi, w.n_kv[t]) - w.lo);
+}
+
+// NANS: a NaN operand gives NaN.
+template <bool NANS = false>
 __device__ __forceinline__ float max3f(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  if constexpr (NANS)
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  else
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <bool NANS = false>
+__device__ __forceinline__ float max2f(float a, float b) {
+  if constexpr (!NANS) return fmaxf(a, b);
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -403,7 +524,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // MMA overlap this item's tail.
 // PAGED: K and V come from a pool of 16-token blocks [num_blocks, Hkv, 16, D]
 // addressed through the block table; the K/V tensor maps then cover the pool.
-template <int D, int EMU8, bool PAGED>
+// SPLIT: for dense keys that the launch before writes; with args.shares an
+// item's key blocks may be shared by several CTAs (split_items), whose partial
+// results a dependent launch merges (split_combine_kernel).
+template <int D, int EMU8, bool PAGED, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     prefill_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -461,12 +585,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   int* item_list = reinterpret_cast<int*>(smem + L::LIST_OFF);
   int* n_mine = reinterpret_cast<int*>(smem + L::MISC_OFF + 8);
-  if (args.sort_items)
+  if (SPLIT && args.shares)
+    split_items<NUM_THREADS>(args, n_items, reinterpret_cast<int*>(smem + L::K_OFF), item_list);
+  else if (args.sort_items)
     order_items(args, n_items, reinterpret_cast<unsigned long long*>(smem + L::K_OFF), item_list, n_mine);
   // The k-th item of this CTA (-1 past its last).
   auto cta_item = [&](int k) -> int {
+    if (SPLIT && args.shares) return k < item_list[4] ? item_list[0] + k : -1;
     if (args.sort_items) return k < *n_mine ? item_list[k] : -1;
     return snake_item(k, n_items);
+  };
+  auto cta_work = [&](int item) -> Work {
+    Work w = decode_work<SPLIT>(args, item);
+    if (SPLIT && args.shares) clip_work(w, item, item_list);
+    return w;
   };
 
   if (warp >= SOFTMAX_WARPS) {
@@ -476,11 +608,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
+      if constexpr (SPLIT) asm volatile("griddepcontrol.wait;" ::: "memory");  // K and V come from the launch before
       int nk = 0, nv = 0;  // K / V blocks issued so far (all items)
       int nq = 0;          // items whose Q was loaded
       bool ok = true;
       for (int kk_item = 0, item; ok && (item = cta_item(kk_item)) >= 0; ++kk_item) {
-        const Work w = decode_work(args, item);
+        const Work w = cta_work(item);
         const int n_kv = max(w.n_kv[0], w.n_kv[1]);
         if (!w.active[0] && !w.active[1]) continue;
         if (PAGED && args.seqlens_k[w.b] > args.max_blocks * 16 && args.error_flags)
@@ -503,7 +636,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         {
           const int nxt = cta_item(kk_item + 1);
           if (nxt >= 0) {
-            const Work wn = decode_work(args, nxt);
+            const Work wn = decode_work<SPLIT>(args, nxt);
             for (int t = 0; t < 2; ++t) {
               if (!wn.active[t]) continue;
               for (int c = 0; c < L::CHUNKS; ++c)
@@ -571,11 +704,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // The tensor core consumes K_0, V_0, K_1, V_1, ...; each load first
         // waits for the block two back in its ring to be released.
         for (int i = 0; i < n_kv && ok; ++i) {
-          fetch_table(i);
-          ok = load(false, i);
-          if (ok) ok = load(true, i);
+          const int blk = SPLIT ? w.lo + i : i;
+          fetch_table(blk);
+          ok = load(false, blk);
+          if (ok) ok = load(true, blk);
         }
       }
+      if constexpr (SPLIT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       // Drain: wait for the last copy issued into each slot (a slot's earlier
       // copy completed before its empty barrier let the next one start), so no
       // copy is in flight when the CTA exits. On the abort path the consumers
@@ -634,7 +769,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int nq = 0;          // active items so far (Q phases)
       bool ok = true;
       for (int kk_item = 0, item; ok && (item = cta_item(kk_item)) >= 0; ++kk_item) {
-        const Work w = decode_work(args, item);
+        const Work w = cta_work(item);
         if (!w.active[0] && !w.active[1]) continue;
         const int n_kv = max(w.n_kv[0], w.n_kv[1]);
         // S of block i for every tile that has it; then K_i can be released.
@@ -719,7 +854,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int nf = 0;  // items this tile finished (o_full phases)
     bool ok = true;
     for (int kk_item = 0, item; ok && (item = cta_item(kk_item)) >= 0; ++kk_item) {
-      const Work w = decode_work(args, item);
+      const Work w = cta_work(item);
       if (!w.active[0] && !w.active[1]) continue;
       const int n_kv = max(w.n_kv[0], w.n_kv[1]);
       const int nt = w.n_kv[t];
@@ -748,7 +883,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float s[BK];
 #pragma unroll
         for (int c = 0; c < BK; ++c) s[c] = __uint_as_float(sb[c]);
-        const int k0 = i * BK;
+        const int k0 = (SPLIT ? w.lo + i : i) * BK;
         const bool need_mask = (k0 + BK > w.sk) || (args.causal && (k0 + BK - 1 > w.row0[t] + (w.sk - w.sq)));
         if (need_mask) {
           const int lim = args.causal ? min(w.sk, qpos + 1) : w.sk;  // keys [0, lim) visible
@@ -756,15 +891,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int c = 0; c < BK; ++c)
             if (k0 + c >= lim) s[c] = -INFINITY;
         }
-        // Row max: eight independent max3 chains.
+        // Row max: eight independent max3 chains. SPLIT: a NaN score (a NaN code
+        // in a visible key) is the maximum, and makes the row's sum NaN below;
+        // the polynomial's clamp would drop it.
         float am[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) am[k] = fmaxf(s[k], s[k + 8]);
+        for (int k = 0; k < 8; ++k) am[k] = max2f<SPLIT>(s[k], s[k + 8]);
 #pragma unroll
         for (int c = 16; c < BK; c += 16)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) am[k] = max3f(am[k], s[c + k], s[c + k + 8]);
-        const float mx = max3f(max3f(am[0], am[1], am[2]), max3f(am[3], am[4], am[5]), fmaxf(am[6], am[7]));
+          for (int k = 0; k < 8; ++k) am[k] = max3f<SPLIT>(am[k], s[c + k], s[c + k + 8]);
+        const float mx = max3f<SPLIT>(max3f<SPLIT>(am[0], am[1], am[2]), max3f<SPLIT>(am[3], am[4], am[5]),
+                                      max2f<SPLIT>(am[6], am[7]));
         const float m_new = fmaxf(m2, mx * sl2);
         const bool upd = (m_new - m2) > RESCALE_THRESHOLD;  // false when both are -inf (NaN compare)
         const float alpha = upd ? ex2_approx(m2 - m_new) : 1.f;
@@ -792,6 +930,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           exp_pack_store<EMU8>(s, sl2, m_off, tS, acc);
         }
         l = l * alpha + (acc.x + acc.y);
+        if (SPLIT && isnan(mx)) l = NAN;
         if (v_fix && i == nt - 1) {
           const int vg = kb + i, vs = vg % VSTAGES;
           ok = warp_wait(&v_full[vs], (vg / VSTAGES) & 1, abort_flag, args.wait_limit);
@@ -822,7 +961,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // ------------------------------------------------------------ epilogue
       // 1 / l and the LSE need no TMEM: done while the last P V runs.
       const bool store = qrow < w.sq;
-      const bool empty = !(l > 0.f);
+      const bool empty = SPLIT ? l == 0.f : !(l > 0.f);
       const float inv_l = empty ? 0.f : 1.f / l;
       // The row, head and batch coordinates of this row's O and LSE (rows
       // past the sequence end are not stored).
@@ -830,7 +969,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           !store || ATTN_IN_BOUNDS(w.qoff + qrow >= 0 && w.qoff + qrow < args.out_rows && w.head[t] >= 0 &&
                                        w.head[t] < args.hq && w.qb >= 0 && w.qb < (args.cu_seqlens_q ? 1 : args.batch),
                                    ATTN_SITE_PREFILL_OUT, args.error_flags, args.planted);
-      if (args.lse && store && out_ok) {
+      // A piece of an item: O (normalised) and LSE go to the CTA's slot of partial results.
+      const bool part = SPLIT && w.part;
+      const long long slot = part ? (2LL * blockIdx.x + (w.lo > 0 ? 0 : 1)) * 2 + t : 0;
+      if (part) {
+        if (store && out_ok) args.part_lse[slot * BM + r] = empty ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994530942f;
+      } else if (args.lse && store && out_ok) {
         const float lse = empty ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994530942f;
         args.lse[((long long)w.qb * args.hq + w.head[t]) * args.lse_rows + w.qoff + qrow] = lse;
       }
@@ -843,7 +987,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const long long obase = (long long)w.qb * args.o_bs + (long long)w.head[t] * args.o_hs +
                               (long long)(w.qoff + qrow) * args.o_rs;
       if (has_keys) tc_fence_after();
-      if (args.o_tma && w.row0[t] + sub * 32 + 32 <= w.sq) {  // warp-uniform
+      if (!part && args.o_tma && w.row0[t] + sub * 32 + 32 <= w.sq) {  // warp-uniform
         uint8_t* stage = smem + L::O_OFF + warp * L::W_STAGE;
         const int r0 = w.qoff + w.row0[t] + sub * 32;
         // The warp's staging area (one 4 KB box per round) and its 32 output
@@ -870,7 +1014,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
         if (!store || !out_ok) continue;
-        if (args.o_f32) {
+        if (part) {
+          float4* dst = reinterpret_cast<float4*>(args.part_o) + (slot * (D / 4) + c * 8) * BM + r;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            dst[k / 4 * BM] = make_float4(__uint_as_float(o[k]) * inv_l, __uint_as_float(o[k + 1]) * inv_l,
+                                          __uint_as_float(o[k + 2]) * inv_l, __uint_as_float(o[k + 3]) * inv_l);
+        } else if (args.o_f32) {
           float* dst = reinterpret_cast<float*>(args.o) + obase + c * 32;
 #pragma unroll
           for (int k = 0; k < 32; k += 4) {
@@ -904,6 +1054,84 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// Merges the pieces of the item that CTA blockIdx.x began and the CTAs behind it
+// continued: O = sum_i e^(lse_i - lse) O_i. A block has 32 rows, a lane a row,
+// a warp every 8th group of 4 columns; O goes out through shared memory. Nearly
+// all items that are cut have two or three pieces; what bounds the kernel is
+// the chain shares - lengths - partial results, so all blocks run at once.
+constexpr int COMBINE_WARPS = 8, COMBINE_ROWS = 32;
+template <int D>
+__global__ void __launch_bounds__(COMBINE_WARPS * 32) split_combine_kernel(const Args args, int n_shares) {
+  constexpr int GROUPS = D / 4 / COMBINE_WARPS;  // groups of columns per warp
+  constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.69314718055994530942f;
+  __shared__ float s_o[COMBINE_ROWS][D + 4];
+  const int c = blockIdx.x, t = blockIdx.y, lane = lane_id();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int item = __ldcg(&args.shares[c].z);
+  // The CTAs that continue the item follow one another; the last one ends it.
+  int n = 1;
+  for (int i0 = c + 1; i0 < n_shares; i0 += 32) {
+    const bool has = i0 + lane < n_shares && __ldcg(&args.shares[i0 + lane].x) == item;
+    const unsigned none = ~__ballot_sync(0xffffffffu, has);
+    n += none ? __ffs(none) - 1 : 32;
+    if (none) break;
+  }
+  if (item < 0) return;
+  const Work w = decode_work<true>(args, item);
+  const int r0 = blockIdx.z * COMBINE_ROWS, r = r0 + lane;
+  const int rows = min(COMBINE_ROWS, w.sq - (w.row0[t] + r0));
+  if (!w.active[t] || rows <= 0) return;
+  float m = -INFINITY, sum = 0.f;
+  float4 acc[GROUPS];
+#pragma unroll
+  for (int k = 0; k < GROUPS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (lane < rows) {
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+      // Piece i: the CTA's second slot, then the first slots of those behind it.
+      const long long slot = (i == 0 ? 2LL * c + 1 : 2LL * (c + i)) * 2 + t;
+      const float4* src = reinterpret_cast<const float4*>(args.part_o) + slot * (D / 4) * BM + r;
+      const float lse = __ldcg(args.part_lse + slot * BM + r);
+      float4 x[GROUPS];
+#pragma unroll
+      for (int k = 0; k < GROUPS; ++k) x[k] = __ldcg(src + (k * COMBINE_WARPS + warp_id()) * BM);
+      const float top = fmaxf(m, lse), ts = top == -INFINITY ? 0.f : top;
+      const float keep = ex2_approx((m - ts) * LOG2E), wgt = ex2_approx((lse - ts) * LOG2E);
+      m = top;
+      sum = fmaf(sum, keep, wgt);
+#pragma unroll
+      for (int k = 0; k < GROUPS; ++k) {
+        acc[k].x = fmaf(wgt, x[k].x, acc[k].x * keep);
+        acc[k].y = fmaf(wgt, x[k].y, acc[k].y * keep);
+        acc[k].z = fmaf(wgt, x[k].z, acc[k].z * keep);
+        acc[k].w = fmaf(wgt, x[k].w, acc[k].w * keep);
+      }
+    }
+  }
+  const bool empty = sum == 0.f;
+  const float inv = empty ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < GROUPS; ++k)
+    *reinterpret_cast<float4*>(&s_o[lane][(k * COMBINE_WARPS + warp_id()) * 4]) =
+        make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
+  if (warp_id() == 0 && lane < rows && args.lse)
+    args.lse[((long long)w.qb * args.hq + w.head[t]) * args.lse_rows + w.qoff + w.row0[t] + r] =
+        empty ? -INFINITY : m + log2f(sum) * LN2;
+  __syncthreads();
+  const long long o0 = (long long)w.qb * args.o_bs + (long long)w.head[t] * args.o_hs +
+                       (long long)(w.qoff + w.row0[t] + r0) * args.o_rs;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += COMBINE_WARPS * 32) {
+    const int row = i / (D / 4), col = i % (D / 4) * 4;
+    const float4 x = *reinterpret_cast<const float4*>(&s_o[row][col]);
+    const long long o = o0 + row * args.o_rs + col;
+    if (args.o_f32)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(args.o) + o) = x;
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(args.o) + o) =
+          make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   }
 }
 
@@ -946,12 +1174,12 @@ static bool encode_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t 
   return r == CUDA_SUCCESS;
 }
 
-template <int D, int EMU8, bool PAGED>
+template <int D, int EMU8, bool PAGED, bool SPLIT = false>
 static attn_status_t launch_variant(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                     const CUtensorMap& to, const Args& a, int items, cudaStream_t stream) {
   using L = Layout<D>;
   static_assert(L::SMEM_BYTES <= 232448, "shared memory budget");
-  auto kern = prefill_fwd_kernel<D, EMU8, PAGED>;
+  auto kern = prefill_fwd_kernel<D, EMU8, PAGED, SPLIT>;
   static DeviceOnce setup;
   const attn_status_t st = setup.run([&]() -> attn_status_t {
     cudaFuncAttributes fa;
@@ -970,6 +1198,30 @@ static attn_status_t launch_variant(const CUtensorMap& tq, const CUtensorMap& tk
   });
   if (st != ATTN_OK) return st;
   const int grid = items < device_sm_count() ? items : device_sm_count();
+  if constexpr (SPLIT) {
+    // Behind the launch that writes K and V, and before the merge: dependent
+    // launches, so that only the data waits.
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(device_sm_count());
+    cfg.blockDim = dim3(NUM_THREADS);
+    cfg.dynamicSmemBytes = L::SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, to, a, items);
+    if (e == cudaSuccess && a.shares) {
+      cfg.gridDim = dim3(device_sm_count(), 2, BM / COMBINE_ROWS);
+      cfg.blockDim = dim3(COMBINE_WARPS * 32);
+      cfg.dynamicSmemBytes = 0;
+      e = cudaLaunchKernelEx(&cfg, split_combine_kernel<D>, a, device_sm_count());
+    }
+    if (e == cudaSuccess) return ATTN_OK;
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
   Args ak = a;
   // Sort only when lengths vary per sequence and every CTA's share fits its list.
   ak.sort_items = (a.seqlens_q || a.seqlens_k || a.cu_seqlens_q) && items <= SORT_MAX_ITEMS &&
@@ -980,7 +1232,31 @@ static attn_status_t launch_variant(const CUtensorMap& tq, const CUtensorMap& tk
 
 }  // namespace prefill
 
-attn_status_t launch_prefill(const attn_prefill_params& p, cudaStream_t stream) {
+// Bytes of the SPLIT kernels' partial results: O, then LSE, then the shares.
+static void split_layout(int head_dim, size_t* lse_at, size_t* shares_at, size_t* total) {
+  const size_t rows = (size_t)device_sm_count() * 4 * prefill::BM;
+  *lse_at = rows * head_dim * sizeof(float);
+  *shares_at = *lse_at + rows * sizeof(float);
+  *total = (*shares_at + device_sm_count() * sizeof(int4) + 255) / 256 * 256;
+}
+
+static long long prefill_items(const attn_prefill_params& p) {
+  const long long group = p.num_q_heads / p.num_kv_heads, blocks = (p.seqlen_q + prefill::BM - 1) / prefill::BM;
+  return group % 2 == 0 ? blocks * p.batch * p.num_kv_heads * (group / 2) : (blocks + 1) / 2 * p.batch * p.num_q_heads;
+}
+
+static bool splits(const attn_prefill_params& p) {
+  return prefill_items(p) <= prefill::SORT_MAX_ITEMS && p.seqlen_k > prefill::SPLIT_MIN_KEYS;
+}
+
+size_t prefill_split_workspace_bytes(const attn_prefill_params& p) {
+  size_t lse_at, shares_at, total;
+  split_layout(p.head_dim, &lse_at, &shares_at, &total);
+  return splits(p) ? total : 0;
+}
+
+static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStream_t stream, bool behind,
+                                         void* split_workspace) {
   using namespace prefill;
   if (p.batch == 0 || p.seqlen_q == 0 || p.num_q_heads == 0) return ATTN_OK;
   const bool paged = p.k_cache != nullptr;
@@ -1024,7 +1300,15 @@ attn_status_t launch_prefill(const attn_prefill_params& p, cudaStream_t stream) 
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.causal = p.causal ? 1 : 0;
   a.pair_heads = (a.group % 2 == 0) ? 1 : 0;
-  if (a.pair_heads) {
+  if (behind && a.pair_heads) {
+    a.fd_outer.init((p.seqlen_q + BM - 1) / BM * (a.group / 2));
+    a.fd_mid.init(a.group / 2);
+    a.fd_inner.init(p.num_kv_heads);
+  } else if (behind) {
+    a.fd_outer.init(((p.seqlen_q + BM - 1) / BM + 1) / 2);
+    a.fd_mid.init(p.num_q_heads);
+    a.fd_inner.init(a.group);
+  } else if (a.pair_heads) {
     a.fd_outer.init(p.batch * p.num_kv_heads * (a.group / 2));
     a.fd_mid.init(a.group / 2);
     a.fd_inner.init(p.num_kv_heads);
@@ -1063,22 +1347,38 @@ attn_status_t launch_prefill(const attn_prefill_params& p, cudaStream_t stream) 
     a.max_blocks = p.max_blocks_per_seq;
     a.num_blocks = p.num_blocks;
   }
-  long long items;
-  if (a.pair_heads)
-    items = (long long)a.n_row_blocks * p.batch * p.num_kv_heads * (a.group / 2);
-  else
-    items = (long long)((a.n_row_blocks + 1) / 2) * p.batch * p.num_q_heads;
+  const long long items = prefill_items(p);
   if (items <= 0) return ATTN_OK;
   if (items > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
 
   // A quarter of the exponentials go to the FMA-pipe polynomial (measured best
   // on B200 for head_dim 128: the MUFU pipe is the scarcer resource).
+  if (behind) {
+    if (splits(p)) {
+      uint8_t* ws = reinterpret_cast<uint8_t*>(split_workspace);
+      size_t lse_at, shares_at, total;
+      split_layout(D, &lse_at, &shares_at, &total);
+      a.part_o = reinterpret_cast<float*>(ws);
+      a.part_lse = reinterpret_cast<float*>(ws + lse_at);
+      a.shares = reinterpret_cast<int4*>(ws + shares_at);
+    }
+    if (D == 128) return launch_variant<128, 2, false, true>(tq, tk, tv, to, a, (int)items, stream);
+    return launch_variant<64, 2, false, true>(tq, tk, tv, to, a, (int)items, stream);
+  }
   if (paged) {
     if (D == 128) return launch_variant<128, 2, true>(tq, tk, tv, to, a, (int)items, stream);
     return launch_variant<64, 2, true>(tq, tk, tv, to, a, (int)items, stream);
   }
   if (D == 128) return launch_variant<128, 2, false>(tq, tk, tv, to, a, (int)items, stream);
   return launch_variant<64, 2, false>(tq, tk, tv, to, a, (int)items, stream);
+}
+
+attn_status_t launch_prefill(const attn_prefill_params& p, cudaStream_t stream) {
+  return launch_prefill_with(p, stream, false, nullptr);
+}
+
+attn_status_t launch_prefill_behind(const attn_prefill_params& p, void* split_workspace, cudaStream_t stream) {
+  return launch_prefill_with(p, stream, true, split_workspace);
 }
 
 }  // namespace attn

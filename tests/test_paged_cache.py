@@ -545,6 +545,51 @@ def test_prefill_block_scaled_bounds_and_empty_rows(lib):
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
+@gpu
+@pytest.mark.parametrize("context", [20, 1500])
+def test_prefill_block_scaled_nan_in_a_visible_key(lib, context):
+    """Rows that see a NaN key give NaN (O and LSE), the rows before it and the other head do not."""
+    n, rows = context + 9, 9
+    for col in range(8):  # every place in a run of columns
+        c = _decode_case([n], 4, 2, 64, 22)
+        at = context + 1 + col % 8
+        c["kc"][int(c["table"][0, at // 16]), 1, at % 16, 3] = 0x7F
+        dev = [c[k].cuda() for k in ("kc", "vc", "ks", "vs", "table")]
+        q = torch.randn(1, 4, rows, 64, generator=_gen(col)).to(torch.bfloat16).cuda()
+        o, lse = lib.prefill_paged_block_scaled(q, *dev, _i32([n]).cuda(), max_seqlen_k=n)
+        sees = torch.arange(context, n) >= at
+        assert torch.isfinite(o[:, :2]).all() and torch.isfinite(lse[:, :2]).all()
+        for h in (2, 3):
+            assert torch.equal(torch.isnan(o[0, h]).all(-1).cpu(), sees) and torch.equal(torch.isnan(lse[0, h]).cpu(), sees)
+            assert torch.isfinite(o[0, h][~sees]).all()
+
+
+@gpu
+@pytest.mark.parametrize("Hq,Hk", [(4, 2), (3, 1)])
+def test_prefill_block_scaled_shared_items(lib, Hq, Hk):
+    """Few rows over long keys: every item's keys are shared by many CTAs, and ragged lengths end inside shares."""
+    D, chunks, lens = 64, [1, 130, 3, 0], [6000, 4100, 3, 900]
+    c = _decode_case(lens, Hq, Hk, D, 23)
+    q = torch.randn(sum(chunks), Hq, D, generator=_gen(24)).to(torch.bfloat16)
+    cu = [0, 1, 131, 134, 134]
+    dev = [c[k].cuda() for k in ("kc", "vc", "ks", "vs", "table")]
+    runs = [lib.prefill_paged_block_scaled(q.cuda(), *dev, _i32(lens).cuda(), cu_seqlens_q=_i32(cu).cuda(), max_seqlen_q=130,
+                                           out_dtype=torch.float32) for _ in range(2)]
+    assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])  # no order of arrival in it
+    kv, vv = ref.values(c["kc"], c["ks"]), ref.values(c["vc"], c["vs"])
+    for b, n in enumerate(lens):
+        rows = chunks[b]
+        ids = c["table"][b, : (n + 15) // 16].long()
+        k, v = (x[ids].transpose(0, 1).reshape(Hk, -1, D)[:, :n] for x in (kv, vv))
+        ev = (c["vs"][ids].double() - 127).T.repeat_interleave(16, 1)[:, :n]
+        qs = q[cu[b]:cu[b + 1]].double().permute(1, 0, 2).reshape(Hk, Hq // Hk * rows, D)
+        limit = torch.arange(n - rows + 1, n + 1).repeat(Hq // Hk)
+        want, wl, tol, ltol = _attention_tol(qs, k, ev, v, c["scale"], limit, 2.0 ** -8 + 2.0 ** -11, 0)
+        got, gl = runs[0][0][cu[b]:cu[b + 1]].transpose(0, 1), runs[0][1][:, cu[b]:cu[b + 1]]
+        _within(got, want.reshape(Hq, rows, D), tol.reshape(Hq, rows, D) + 2.0 ** -20 * want.reshape(Hq, rows, D).abs(), f"O {b}")
+        _within(gl, wl.reshape(Hq, rows), ltol.reshape(Hq, rows) + 2.0 ** -12, f"LSE {b}")
+
+
 # ---------------------------------------------------------------------------- together
 
 
