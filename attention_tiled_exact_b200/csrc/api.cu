@@ -357,15 +357,14 @@ attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* p, const 
   attn_status_t st = attn::validate_decode_block_scaled(p, k_scales, v_scales);
   if (st != ATTN_OK) return st;
   const bool have_dev = attn::check_device() == ATTN_OK;
-  const attn::DecodePlan plan = attn::plan_decode_block_scaled(*p);
-  if (workspace_needed) *workspace_needed = plan.workspace_bytes;
+  const size_t need = attn::decode_block_scaled_workspace_bytes(*p);
+  if (workspace_needed) *workspace_needed = need;
   if (workspace == nullptr && workspace_needed != nullptr) return ATTN_OK;  // size query only
-  if (workspace_bytes < plan.workspace_bytes) return ATTN_ERR_WORKSPACE;
-  if (plan.workspace_bytes > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return ATTN_ERR_WORKSPACE;
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_UNSUPPORTED;
   if (p->batch == 0) return ATTN_OK;
   if (!have_dev) return ATTN_ERR_NO_DEVICE;
-  return attn::launch_decode_block_scaled(*p, k_scales, v_scales, plan, workspace,
-                                          reinterpret_cast<cudaStream_t>(stream));
+  return attn::launch_decode_block_scaled(*p, k_scales, v_scales, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 attn_status_t attn_prefill_paged_block_scaled(const attn_prefill_params* p, const uint8_t* k_scales,

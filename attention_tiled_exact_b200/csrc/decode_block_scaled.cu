@@ -1,5 +1,6 @@
-// Single-token attention over the block-scaled 8-bit cache
-// (attn_decode_paged_block_scaled), for sm_100a.
+// Attention of few query rows over the block-scaled 8-bit cache, for sm_100a:
+// single tokens (attn_decode_paged_block_scaled) and short chunks
+// (attn_prefill_paged_block_scaled where its tensor-core tiles would stand empty).
 //
 //   x_j = scale * (q . code_kj) 2^(ek_j),  O = sum_j 2^(ev_j) e^(x_j) code_vj / sum_j e^(x_j)
 // with one exponent ek, ev for each 16-token block. A key's exponent multiplies
@@ -11,14 +12,23 @@
 // a sequence's blocks lie apart. Both maxima are kept stale until they grow by
 // 2^8.
 //
-// One CTA of 4 warps handles one split of one (sequence, kv head), so a block is
-// read from HBM once for the group. Each warp walks every 4th block: K and V
-// codes come through a per-warp ring of cp.async stages, are widened exactly to
-// fp16 (cvt.rn.f16x2.e4m3x2) and go to mma.sync m16n8k16 with fp32 sums. Both
+// A tile is up to 8 * HALVES query rows of one sequence and kv head (row i: token
+// i / group, head i % group); a block is read from HBM once for the tile. The
+// keys that a tile sees are dealt out evenly to the CTAs of a row of the grid,
+// by the sequence's own length, so that every CTA of a sequence ends with the
+// others. CLUSTER of them are a thread-block cluster and merge their results
+// through distributed shared memory. Where that is the whole row of the grid,
+// nothing goes through global memory and no second launch is needed (it cost
+// 3 us of the 11 us of one sequence of 4097 tokens); a longer row, for few long
+// sequences, leaves one partial result per cluster to a dependent launch.
+//
+// The 4 warps of a CTA walk every 4th block of a piece: K and V codes come
+// through a per-warp ring of cp.async stages, are widened exactly to fp16
+// (cvt.rn.f16x2.e4m3x2) and go to mma.sync m16n8k16 with fp32 sums. Both
 // products are computed transposed, S' = K q' and O' = V' P', with the tokens or
-// the elements as the 16 rows and the group's heads as the 8 columns: half the
-// products of the other order, which would pad a group of 8 to 16 rows. P'
-// changes its lane layout between the two with movmatrix.
+// the elements as the 16 rows and the query rows as the 8 columns: half the
+// products of the other order, which would pad 8 query rows to 16. P' changes
+// its lane layout between the two with movmatrix.
 // The ring's 16-byte chunks are swizzled so that the K reads (a row per 4 lanes)
 // and the V reads (a column slice per 8 lanes) are free of bank conflicts.
 // The running maxima move only when some lane's score exceeds them by 2^8: one
@@ -27,11 +37,14 @@
 // brings its largest element into [2^14, 2^15), and the scores are scaled back,
 // so that no bf16 query overflows (elements 2^29 below the row's largest one
 // round to fp16's step there, 2^-39 of the largest).
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
+
+#include <algorithm>
 
 #include "block_scaled.cuh"
 #include "bounds_check.cuh"
@@ -41,10 +54,16 @@
 namespace attn {
 namespace bsdecode {
 
+namespace cg = cooperative_groups;
+
 constexpr int BS = 16;
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int STAGES = 3;
+constexpr int CLUSTER = 8;      // CTAs that merge through shared memory, at most
+// Cache blocks: the least that a CTA is started for (2 per warp), the least per
+// CTA of a row of several clusters, and the pieces of a grid of many rounds.
+constexpr int MIN_BLOCKS = 8, LONG_BLOCKS = 32, EVEN_BLOCKS = 256;
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -58,25 +77,37 @@ struct Args {
   const uint8_t* v_scales;
   const int32_t* block_table;
   const int32_t* seq_lens;
+  const int32_t* cu_q;      // packed queries: sequence b has rows cu_q[b] .. cu_q[b + 1] - 1 of total_q
+  const int32_t* q_lens;    // padded queries: rows of each sequence (NULL: max_q)
   void* o;
   float* lse;
-  int o_f32;
-  float* part_o;    // [split][row][D], normalised
-  float* part_lse;  // [split][row], natural log
-  int batch, hq, hkv, group, max_blocks, num_blocks, split_tokens;
+  long long q_bs, q_hs, q_rs, o_bs, o_hs, o_rs, lse_bs, lse_hs;  // the LSE's row stride is 1
+  float* part_o;    // [cluster][tile of the grid][row][D], normalised
+  float* part_lse;  // [cluster][tile of the grid][row], natural log
+  int o_f32, causal;
+  int batch, max_q, total_q, hkv, group, max_blocks, num_blocks, max_len;
+  int tiles;        // row tiles per sequence and kv head (a bound)
   float scale_log2;
   int32_t* error_flags;
   int planted;
 };
 
+// CTAs per SM that the kernels are built for.
+template <int D, int HALVES>
+constexpr int ctas_per_sm() {
+  return HALVES == 2 ? 3 : D == 128 ? 4 : 5;
+}
 template <int D>
 struct Ring {
   uint8_t kv[WARPS][STAGES][2][BS * D];
 };
 template <int D, int ROWS>
-struct Merge {
+struct Merge {  // over the ring, when it is empty
   float m[WARPS][ROWS], r[WARPS][ROWS], l[WARPS][ROWS];
   float o[WARPS][ROWS][D];
+  // The CTA's result: O in units of 2^r, for the other CTAs of its cluster to read.
+  float cta_m[ROWS], cta_r[ROWS], cta_l[ROWS];
+  float cta_o[ROWS][D];
 };
 template <int D, int ROWS>
 constexpr int smem_bytes() {
@@ -129,43 +160,95 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// The cached tokens that sequence b's call sees: its length, bounded to its
-// table and to the plan's splits (flagged where it was longer or negative).
-__device__ __forceinline__ int bounded_len(const Args& a, int b, int max_splits, bool flag) {
-  int len = __ldg(a.seq_lens + b);
-  const int cap = (int)min((long long)a.max_blocks * BS, (long long)max_splits * a.split_tokens);
-  if (len < 0 || len > cap) {
-    if (flag && a.error_flags) atomicOr(a.error_flags, ATTN_FAULT_BAD_LENGTH);
-    len = len < 0 ? 0 : cap;
+// Tile blockIdx.z % tiles of sequence blockIdx.z / tiles, for every kv head.
+struct Group {
+  int b, row0, rows;  // rows of the tile (0: the sequence has no such tile)
+  int seq, first;     // the sequence's batch coordinate and first row in the q, O and LSE tensors
+  int len, n_q;       // cached tokens, query tokens
+  int blocks;         // key blocks that the tile's last row sees
+  int per_cta, used;  // of them for a CTA of the row of the grid, and CTAs that have some
+};
+
+template <int ROWS>
+__device__ __forceinline__ Group group_of(const Args& a, int gi, int ctas) {
+  Group g;
+  g.b = a.tiles == 1 ? gi : gi / a.tiles;
+  g.row0 = (gi - g.b * a.tiles) * ROWS;
+  g.len = min(max(__ldg(a.seq_lens + g.b), 0), a.max_len);
+  if (a.cu_q) {
+    const int s0 = min(max(__ldg(a.cu_q + g.b), 0), a.total_q);
+    g.n_q = min(max(__ldg(a.cu_q + g.b + 1), s0), a.total_q) - s0;
+    g.seq = 0, g.first = s0;
+  } else {
+    g.seq = g.b, g.first = 0;
+    g.n_q = a.q_lens ? max(__ldg(a.q_lens + g.b), 0) : a.max_q;
   }
-  return len;
+  g.n_q = min(g.n_q, a.max_q);
+  g.rows = max(0, min(ROWS, g.n_q * a.group - g.row0));
+  int end = g.len;
+  if (a.causal) end = min(end, g.len - g.n_q + (g.row0 + g.rows - 1) / a.group + 1);
+  g.blocks = (max(end, 0) + BS - 1) / BS;
+  // At least MIN_BLOCKS each, and as many for every warp.
+  g.per_cta = max(MIN_BLOCKS, ((g.blocks + ctas - 1) / ctas + WARPS - 1) / WARPS * WARPS);
+  g.used = max(1, (g.blocks + g.per_cta - 1) / g.per_cta);
+  return g;
 }
 
-template <typename T>
-__device__ __forceinline__ T* o_row(const Args& a, int b, int head, int d) {
-  return reinterpret_cast<T*>(a.o) + ((long long)b * a.hq + head) * d;
+// Elements d .. d + 3 of the output of row i of a tile, and with element 0 its LSE.
+__device__ __forceinline__ void store_row4(const Args& a, const Group& g, int kvh, int i, int d, float4 o, float lse) {
+  const int token = g.first + (g.row0 + i) / a.group, head = kvh * a.group + (g.row0 + i) % a.group;
+  const long long at = g.seq * a.o_bs + head * a.o_hs + token * a.o_rs + d;
+  if (a.o_f32)
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.o) + at) = o;
+  else
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + at) =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (d == 0 && a.lse) a.lse[g.seq * a.lse_bs + head * a.lse_hs + token] = lse;
 }
 
-// HALVES: groups of 8 columns that hold query heads (group <= 8 * HALVES).
-template <int D, int HALVES>
-__global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(const Args a) {
+__device__ __forceinline__ void add_scaled(float4& acc, float w, const float4& x) {
+  acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
+}
+
+// A row's sum and O (in units of 2^R, its sum in units of 2^M) as output and LSE.
+__device__ __forceinline__ float finish_row(float M, float R, float sum, float4& acc) {
+  const float Ms = M == -INFINITY ? 0.f : M, Rs = R == -INFINITY ? 0.f : R;
+  const bool empty = sum == 0.f;  // a NaN is not an empty row
+  const float inv = empty ? 0.f : 1.f / sum;
+  const float back = exp2f(0.5f * (Rs - Ms));  // applied twice: 2^(R - M) may leave fp32 where O does not
+  acc.x = empty ? 0.f : acc.x * inv * back * back;
+  acc.y = empty ? 0.f : acc.y * inv * back * back;
+  acc.z = empty ? 0.f : acc.z * inv * back * back;
+  acc.w = empty ? 0.f : acc.w * inv * back * back;
+  return empty ? -INFINITY : (Ms + log2f(sum)) * LN2;
+}
+
+// CTAs of a cluster: the row of the grid up to CLUSTER.
+__device__ __forceinline__ int cluster_size() { return min((int)gridDim.x, CLUSTER); }
+
+template <int D, int HALVES, bool CLUSTERED>
+__global__ void __launch_bounds__(THREADS, ctas_per_sm<D, HALVES>()) few_rows_kernel(const Args a) {
   constexpr int ROWS = 8 * HALVES;
   constexpr int KSTEPS = D / 16, MT = D / 16;
   constexpr int COPIES = BS * D / (16 * 32);  // 16-byte copies per lane and block
   extern __shared__ __align__(128) uint8_t smem[];
   Ring<D>& ring = *reinterpret_cast<Ring<D>*>(smem);
-  const int split = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z, max_splits = gridDim.x;
   const int warp = warp_id(), lane = lane_id();
   const int gq = lane >> 2, tq = lane & 3;
-
-  const int T = a.split_tokens;
-  const int L = bounded_len(a, b, max_splits, split == 0 && kvh == 0 && threadIdx.x == 0);
-  const int n_splits = max(1, (L + T - 1) / T);
-  if (split >= n_splits) return;
-  const int t_begin = split * T, t_end = min(L, t_begin + T);
-  const int blk_begin = t_begin / BS, blk_end = (t_end + BS - 1) / BS;
+  const int split = blockIdx.x, kvh = blockIdx.y;
+  const Group grp = group_of<ROWS>(a, blockIdx.z, gridDim.x);
+  const int b = grp.b;
+  if (split == 0 && kvh == 0 && threadIdx.x == 0 && a.error_flags &&
+      (unsigned)__ldg(a.seq_lens + b) > (unsigned)a.max_len)
+    atomicOr(a.error_flags, ATTN_FAULT_BAD_LENGTH);
+  // Without rows, or the whole cluster without keys (the first one writes the rows of none).
+  if (grp.rows == 0 || (CLUSTERED ? split / cluster_size() * cluster_size() : split) >= grp.used) return;
+  const int blk_begin = min(grp.blocks, split * grp.per_cta), blk_end = min(grp.blocks, blk_begin + grp.per_cta);
   const int n_mine = max(0, (blk_end - blk_begin - warp + WARPS - 1) / WARPS);
   const int32_t* table = a.block_table + (long long)b * a.max_blocks;
+  // Row i of the tile: its token and head, and the keys that it sees.
+  auto token_of = [&](int i) { return (grp.row0 + i) / a.group; };
+  auto head_of = [&](int i) { return kvh * a.group + (grp.row0 + i) % a.group; };
 
   // Lane i holds the table entry of this warp's block 32 k + i: one batch of 32
   // is in use for issuing copies, the next one is on its way.
@@ -215,19 +298,21 @@ __global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(con
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) issue(s);
 
-  // B fragments of q: head gq (and gq + 8), elements (D / 4) tq + 4 step + 0..3,
+  // B fragments of q: row gq (and gq + 8), elements (D / 4) tq + 4 step + 0..3,
   // the order in which the lane reads its K row slices.
   uint32_t qb[HALVES][KSTEPS][2];
-  float mul[HALVES][2];  // score of the scaled query of heads 2 tq, 2 tq + 1 (+ 8 h) -> log2 units
+  float mul[HALVES][2];  // score of the scaled query of rows 2 tq, 2 tq + 1 (+ 8 h) -> log2 units
+  int limit[HALVES][2];  // keys that these rows see
 #pragma unroll
   for (int h = 0; h < HALVES; ++h) {
     const int g = gq + 8 * h;
-    const __nv_bfloat16* src = a.q + ((long long)b * a.hq + kvh * a.group + g) * D + (D / 4) * tq;
+    const __nv_bfloat16* src =
+        a.q + grp.seq * a.q_bs + (grp.first + token_of(g)) * a.q_rs + head_of(g) * a.q_hs + (D / 4) * tq;
     uint32_t w[D / 8];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint4 r = make_uint4(0u, 0u, 0u, 0u);
-      if (g < a.group) r = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      if (g < grp.rows) r = __ldg(reinterpret_cast<const uint4*>(src) + i);
       w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
     }
     float top = 0.f;
@@ -241,7 +326,10 @@ __global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(con
     const float up = top > 0.f ? bscale::pow2i(e) : 1.f;
     const float back = a.scale_log2 * (top > 0.f ? bscale::pow2i(-e) : 1.f);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) mul[h][j] = __shfl_sync(FULL, back, 4 * (2 * tq + j));
+    for (int j = 0; j < 2; ++j) {
+      mul[h][j] = __shfl_sync(FULL, back, 4 * (2 * tq + j));
+      limit[h][j] = a.causal ? min(grp.len, grp.len - grp.n_q + token_of(2 * tq + j + 8 * h) + 1) : grp.len;
+    }
 #pragma unroll
     for (int ks = 0; ks < KSTEPS; ++ks)
 #pragma unroll
@@ -251,7 +339,7 @@ __global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(con
       }
   }
 
-  // O of element (D / 8) gq + 2 mt + i / 2, head 2 tq + i % 2 (+ 8 h) in ot[h][mt][i], in units of 2^r.
+  // O of element (D / 8) gq + 2 mt + i / 2, row 2 tq + i % 2 (+ 8 h) in ot[h][mt][i], in units of 2^r.
   float ot[HALVES][MT][4];
   float m[HALVES][2], r[HALVES][2], l[HALVES][2];  // l: this lane's tokens only, until the end
 #pragma unroll
@@ -272,11 +360,12 @@ __global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(con
     // of 32 before this side does.
     if ((n & 31) == 0) sc_use = sc_issue;
     const int sc = __shfl_sync(FULL, sc_use, n & 31);
-    const int n_valid = sc < 0 ? 0 : min(BS, t_end - (blk_begin + warp + n * WARPS) * BS);
+    const int tok0 = (blk_begin + warp + n * WARPS) * BS;
+    const int n_valid = sc < 0 ? 0 : min(BS, grp.len - tok0);
     if (n_valid > 0) {
       const uint8_t* kblk = ring.kv[warp][n % STAGES][0];
       const uint8_t* vblk = ring.kv[warp][n % STAGES][1];
-      // ---- S' = K q': tokens gq (x[h][0], x[h][1]: heads 2 tq, 2 tq + 1) and gq + 8 (x[h][2], x[h][3])
+      // ---- S' = K q': tokens gq (x[h][0], x[h][1]: rows 2 tq, 2 tq + 1) and gq + 8 (x[h][2], x[h][3])
       float x[HALVES][4];
 #pragma unroll
       for (int h = 0; h < HALVES; ++h)
@@ -310,8 +399,8 @@ __global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(con
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float f = mul[h][j] * k_mul;
-          x[h][j] = gq < n_valid ? x[h][j] * f : -INFINITY;
-          x[h][2 + j] = gq + 8 < n_valid ? x[h][2 + j] * f : -INFINITY;
+          x[h][j] = tok0 + gq < limit[h][j] ? x[h][j] * f : -INFINITY;
+          x[h][2 + j] = tok0 + gq + 8 < limit[h][j] ? x[h][2 + j] * f : -INFINITY;
           const float top = fmaxf(x[h][j], x[h][2 + j]);
           over |= top - m[h][j] > RESCALE_THRESHOLD || top + ev - r[h][j] > RESCALE_THRESHOLD;
         }
@@ -409,55 +498,91 @@ __global__ void __launch_bounds__(THREADS, HALVES == 1 ? 4 : 3) split_kernel(con
       for (int mt = 0; mt < MT; ++mt) dst[mt] = make_float2(ot[h][mt][j], ot[h][mt][2 + j]);
     }
   __syncthreads();
-  const long long rows = (long long)a.batch * a.hq;
-  for (int i = threadIdx.x; i < a.group * D; i += THREADS) {
-    const int g = i / D, d = i % D;
+  for (int i = threadIdx.x; i < grp.rows * (D / 4); i += THREADS) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
     float M = -INFINITY, R = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mg.m[w][g]), R = fmaxf(R, mg.r[w][g]);
+    for (int w = 0; w < WARPS; ++w) M = fmaxf(M, mg.m[w][row]), R = fmaxf(R, mg.r[w][row]);
     const float Ms = M == -INFINITY ? 0.f : M, Rs = R == -INFINITY ? 0.f : R;
-    float sum = 0.f, acc = 0.f;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      sum = fmaf(ex2_approx(mg.m[w][g] - Ms), mg.l[w][g], sum);
-      acc = fmaf(ex2_approx(mg.r[w][g] - Rs), mg.o[w][g][d], acc);
+      sum = fmaf(ex2_approx(mg.m[w][row] - Ms), mg.l[w][row], sum);
+      add_scaled(acc, ex2_approx(mg.r[w][row] - Rs), *reinterpret_cast<const float4*>(&mg.o[w][row][d]));
     }
-    const bool empty = sum == 0.f;  // a NaN is not an empty row
-    const float back = exp2f(0.5f * (Rs - Ms));  // applied twice: 2^(R - M) may leave fp32 where O does not
-    const float out = empty ? 0.f : acc / sum * back * back;
-    const float lse = empty ? -INFINITY : (Ms + log2f(sum)) * LN2;
-    const int head = kvh * a.group + g;
-    const long long row = (long long)b * a.hq + head;
-    if (n_splits == 1) {
-      if (a.o_f32)
-        o_row<float>(a, b, head, D)[d] = out;
-      else
-        o_row<__nv_bfloat16>(a, b, head, D)[d] = __float2bfloat16_rn(out);
-      if (d == 0 && a.lse) a.lse[row] = lse;
-    } else if (ATTN_IN_BOUNDS(split >= 0 && split < max_splits && row >= 0 && row < rows, ATTN_SITE_DECODE_PARTIAL,
-                              a.error_flags, a.planted)) {
-      a.part_o[((long long)split * rows + row) * D + d] = out;
-      if (d == 0) a.part_lse[(long long)split * rows + row] = lse;
+    if constexpr (CLUSTERED) {
+      *reinterpret_cast<float4*>(&mg.cta_o[row][d]) = acc;
+      if (d == 0) mg.cta_m[row] = M, mg.cta_r[row] = R, mg.cta_l[row] = sum;
+    } else {
+      const float lse = finish_row(M, R, sum, acc);
+      store_row4(a, grp, kvh, row, d, acc, lse);
     }
+  }
+  if constexpr (CLUSTERED) {
+    // ---- merge the cluster: each CTA a part of the rows' elements
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), first = split - rank;
+    const int size = cluster_size(), n = min(size, grp.used - first);  // CTAs of the cluster with keys, or the first one
+    const bool part = grp.used > CLUSTER;
+    cluster.sync();
+    for (int i = threadIdx.x * size + rank; i < grp.rows * (D / 4); i += size * THREADS) {
+      const int row = i / (D / 4), d = i % (D / 4) * 4;
+      float m[CLUSTER], r[CLUSTER], l[CLUSTER];
+      float4 o[CLUSTER];
+      float M = -INFINITY, R = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < CLUSTER; ++c) {
+        m[c] = r[c] = -INFINITY;
+        l[c] = 0.f;
+        o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < n) {
+          const Merge<D, ROWS>& of = *cluster.map_shared_rank(&mg, c);
+          m[c] = of.cta_m[row], r[c] = of.cta_r[row], l[c] = of.cta_l[row];
+          o[c] = *reinterpret_cast<const float4*>(&of.cta_o[row][d]);
+        }
+        M = fmaxf(M, m[c]), R = fmaxf(R, r[c]);
+      }
+      const float Ms = M == -INFINITY ? 0.f : M, Rs = R == -INFINITY ? 0.f : R;
+      float sum = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < CLUSTER; ++c) {
+        sum = fmaf(ex2_approx(m[c] - Ms), l[c], sum);
+        add_scaled(acc, ex2_approx(r[c] - Rs), o[c]);
+      }
+      const float lse = finish_row(M, R, sum, acc);
+      if (!part) {
+        store_row4(a, grp, kvh, row, d, acc, lse);
+      } else {
+        const long long at = (((long long)(split / CLUSTER) * gridDim.z + blockIdx.z) * a.hkv + kvh) * ROWS + row;
+        if (ATTN_IN_BOUNDS(split / CLUSTER < (int)gridDim.x / CLUSTER && row < ROWS, ATTN_SITE_DECODE_PARTIAL,
+                           a.error_flags, a.planted)) {
+          *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
+          if (d == 0) a.part_lse[at] = lse;
+        }
+      }
+    }
+    cluster.sync();  // the others have read this CTA's shared memory
   }
 }
 
-// One block per row of more than one split: O = sum_s e^(lse_s - lse) O_s, the
-// splits dealt out to 4 warps. A dependent launch: it is set up while the last
-// splits run.
-template <int D>
-__global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int max_splits) {
+// Merges the clusters' partial results of one row (blockIdx.x) of one tile and kv
+// head: O = sum_s e^(lse_s - lse) O_s, dealt out to 4 warps. A dependent launch:
+// it is set up while the last splits run.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int ctas) {
   constexpr int PER = D / 32;
-  __shared__ float s_m[WARPS], s_sum[WARPS], s_acc[WARPS][D];
-  const int row = blockIdx.x, b = row / a.hq, warp = warp_id(), lane = lane_id();
-  const int T = a.split_tokens, L = bounded_len(a, b, max_splits, false);
-  const int n = (L + T - 1) / T;
+  __shared__ float s_m[WARPS], s_sum[WARPS];
+  __shared__ __align__(16) float s_acc[WARPS][D];
+  const int row = blockIdx.x, kvh = blockIdx.y, warp = warp_id(), lane = lane_id();
+  const Group grp = group_of<ROWS>(a, blockIdx.z, ctas);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (n <= 1) return;
-  const long long rows = (long long)a.batch * a.hq;
-  const float* lse = a.part_lse + row;
+  if (row >= grp.rows || grp.used <= CLUSTER) return;
+  const int n = (grp.used + CLUSTER - 1) / CLUSTER;
+  const long long first = ((long long)blockIdx.z * a.hkv + kvh) * ROWS + row, step = (long long)gridDim.z * a.hkv * ROWS;
   float M = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += THREADS) M = fmaxf(M, __ldcg(lse + s * rows));
+  for (int i = threadIdx.x; i < n; i += THREADS) M = fmaxf(M, __ldcg(a.part_lse + first + i * step));
 #pragma unroll
   for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, d));
   if (lane == 0) s_m[warp] = M;
@@ -469,9 +594,10 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int max_
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll 4
-  for (int s = warp; s < n; s += WARPS) {
-    const float w = ex2_approx((__ldcg(lse + s * rows) - Ms) * LOG2E);
-    const float* src = a.part_o + (s * rows + row) * D + lane * PER;
+  for (int i = warp; i < n; i += WARPS) {
+    if (!ATTN_IN_BOUNDS(i < ctas / CLUSTER, ATTN_SITE_COMBINE, a.error_flags, a.planted)) break;
+    const float w = ex2_approx((__ldcg(a.part_lse + first + i * step) - Ms) * LOG2E);
+    const float* src = a.part_o + (first + i * step) * D + lane * PER;
     float x[PER];
     if constexpr (PER == 4) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
@@ -482,33 +608,53 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int max_
     }
     sum += w;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = fmaf(w, x[i], acc[i]);
+    for (int k = 0; k < PER; ++k) acc[k] = fmaf(w, x[k], acc[k]);
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) s_acc[warp][lane * PER + i] = acc[i];
+  for (int k = 0; k < PER; ++k) s_acc[warp][lane * PER + k] = acc[k];
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
+  const int d = threadIdx.x * 4;
+  if (d >= D) return;
   sum = 0.f;
+  float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) sum += s_sum[w];
-  const bool empty = sum == 0.f;
-  if (threadIdx.x < D) {
-    float out = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) out += s_acc[w][threadIdx.x];
-    out = empty ? 0.f : out / sum;
-    if (a.o_f32)
-      reinterpret_cast<float*>(a.o)[(long long)row * D + threadIdx.x] = out;
-    else
-      reinterpret_cast<__nv_bfloat16*>(a.o)[(long long)row * D + threadIdx.x] = __float2bfloat16_rn(out);
+  for (int w = 0; w < WARPS; ++w) {
+    sum += s_sum[w];
+    add_scaled(out, 1.f, *reinterpret_cast<const float4*>(&s_acc[w][d]));
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[row] = empty ? -INFINITY : Ms + log2f(sum) * LN2;
+  // The weights are powers of e relative to Ms: in powers of two for finish_row.
+  const float lse = finish_row(Ms * LOG2E, Ms * LOG2E, sum, out);
+  store_row4(a, grp, kvh, row, d, out, lse);
 }
 
-template <int D, int HALVES>
-static attn_status_t launch(const Args& a, int max_splits, cudaStream_t stream) {
-  constexpr int SMEM = smem_bytes<D, 8 * HALVES>();
-  auto kern = split_kernel<D, HALVES>;
+// CTAs in a row of the grid. Enough that the grid fills the machine once, and
+// not a second time in part (8 sequences of 4096 tokens, 64 tiles: 8 CTAs each
+// 17 us, 4 CTAs 18 us, 16 CTAs 25 us; 32 of 2048, 256 tiles: 2 CTAs 28 us, 1 CTA
+// 30 us, 4 CTAs 32 us). A grid that is larger anyway is cut into
+// pieces of EVEN_BLOCKS, so that a long sequence at its end does not run alone
+// (64 sequences of 1K to 32K tokens, 512 tiles: 8 CTAs 325 us, 4 CTAs 333 us,
+// 1 CTA 470 us, 16 CTAs 364 us). A row of more than one cluster costs a merge through
+// memory and is taken for LONG_BLOCKS per CTA (one sequence of 32768 tokens
+// and one kv head: 64 CTAs 12 us, 8 CTAs 45 us).
+static int ctas_per_tile(const Args& a, int num_splits, int slots) {
+  const long long blocks = (a.max_len + BS - 1) / BS, tiles = (long long)a.batch * a.tiles * a.hkv;
+  long long n = num_splits;
+  if (n == 0) {
+    n = slots / tiles;
+    if (n <= CLUSTER) n = std::max(n, std::min<long long>(CLUSTER, blocks / EVEN_BLOCKS));
+    n = std::min(n, std::max(blocks / LONG_BLOCKS, std::min<long long>(CLUSTER, blocks / MIN_BLOCKS)));
+  } else {
+    n = std::min(n, std::max(1ll, blocks / MIN_BLOCKS));
+  }
+  if (n > CLUSTER) return (int)(n / CLUSTER * CLUSTER);
+  return n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
+}
+
+template <int D, int HALVES, bool CLUSTERED>
+static attn_status_t launch_grid(const Args& a, int ctas, cudaStream_t stream) {
+  constexpr int ROWS = 8 * HALVES, SMEM = smem_bytes<D, ROWS>();
+  auto kern = few_rows_kernel<D, HALVES, CLUSTERED>;
   static DeviceOnce setup;
   const attn_status_t st = setup.run([&]() -> attn_status_t {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
@@ -518,87 +664,148 @@ static attn_status_t launch(const Args& a, int max_splits, cudaStream_t stream) 
     return ATTN_OK;
   });
   if (st != ATTN_OK) return st;
-  kern<<<dim3(max_splits, a.hkv, a.batch), THREADS, SMEM, stream>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
-  if (max_splits <= 1) return ATTN_OK;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(a.batch * a.hq);
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas < CLUSTER ? ctas : CLUSTER;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas, a.hkv, a.batch * a.tiles);
   cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, combine_kernel<D>, a, max_splits) != cudaSuccess) {
-    cudaGetLastError();
-    return ATTN_ERR_CUDA;
+  cfg.numAttrs = CLUSTERED ? 1 : 0;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e == cudaSuccess && ctas > CLUSTER) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    const long long rows = (long long)a.max_q * a.group;
+    cfg.gridDim = dim3(rows < ROWS ? (int)rows : ROWS, a.hkv, a.batch * a.tiles);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<D, ROWS>, a, ctas);
   }
-  return ATTN_OK;
+  if (e == cudaSuccess) return ATTN_OK;
+  cudaGetLastError();
+  return ATTN_ERR_CUDA;
 }
 
-}  // namespace bsdecode
-
-DecodePlan plan_decode_block_scaled(const attn_decode_params& p) {
-  using namespace bsdecode;
-  DecodePlan plan;
-  const int cap = p.max_blocks_per_seq * BS;
-  const int max_len = p.max_seq_len > 0 && p.max_seq_len < cap ? p.max_seq_len : cap;
-  constexpr int UNIT = BS * WARPS;
-  int T;
-  if (p.num_splits > 0) {
-    T = (max_len + p.num_splits - 1) / p.num_splits;
-  } else {
-    const long long pairs = (long long)p.batch * p.num_kv_heads;
-    long long per_seq = pairs > 0 ? (32LL * device_sm_count() + pairs - 1) / pairs : 1;
-    T = (int)((max_len + per_seq - 1) / per_seq);
-    if (T < 512) T = 512;
+// With `bytes` only the workspace's size: O, then LSE of the partial results.
+template <int D, int HALVES>
+static attn_status_t launch(Args a, int num_splits, void* workspace, size_t* bytes, cudaStream_t stream) {
+  constexpr int ROWS = 8 * HALVES;
+  a.tiles = (int)(((long long)a.max_q * a.group + ROWS - 1) / ROWS);
+  const int ctas = ctas_per_tile(a, num_splits, device_sm_count() * ctas_per_sm<D, HALVES>());
+  const size_t n = ctas > CLUSTER ? (size_t)(ctas / CLUSTER) * a.batch * a.tiles * a.hkv * ROWS : 0;
+  const size_t lse_at = n * D * sizeof(float);
+  if (bytes) {
+    *bytes = (lse_at + n * sizeof(float) + 255) / 256 * 256;
+    return ATTN_OK;
   }
-  T = (T + UNIT - 1) / UNIT * UNIT;
-  plan.split_tokens = T;
-  plan.max_splits = (max_len + T - 1) / T;
-  const size_t rows = (size_t)p.batch * p.num_q_heads;
-  const size_t po = (plan.max_splits * rows * p.head_dim * sizeof(float) + 255) / 256 * 256;
-  const size_t pl = (plan.max_splits * rows * sizeof(float) + 255) / 256 * 256;
-  plan.workspace_bytes = plan.max_splits > 1 ? po + pl : 0;
-  return plan;
+  a.part_o = reinterpret_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + lse_at);
+  return ctas > 1 ? launch_grid<D, HALVES, true>(a, ctas, stream) : launch_grid<D, HALVES, false>(a, ctas, stream);
 }
 
-attn_status_t launch_decode_block_scaled(const attn_decode_params& p, const uint8_t* k_scales, const uint8_t* v_scales,
-                                         const DecodePlan& plan, void* workspace, cudaStream_t stream) {
-  using namespace bsdecode;
+// Launches, or with `bytes` only gives the workspace's size.
+static attn_status_t dispatch(const Args& a, int head_dim, int num_splits, void* workspace, size_t* bytes, cudaStream_t stream) {
+  const bool wide = (long long)a.max_q * a.group > 8;
+  if (head_dim == 128)
+    return wide ? launch<128, 2>(a, num_splits, workspace, bytes, stream) : launch<128, 1>(a, num_splits, workspace, bytes, stream);
+  return wide ? launch<64, 2>(a, num_splits, workspace, bytes, stream) : launch<64, 1>(a, num_splits, workspace, bytes, stream);
+}
+
+static Args decode_args(const attn_decode_params& p, const uint8_t* k_scales, const uint8_t* v_scales) {
   Args a;
   memset(&a, 0, sizeof(a));
   a.q = reinterpret_cast<const __nv_bfloat16*>(p.q);
   a.k_cache = reinterpret_cast<const uint8_t*>(p.k_cache);
   a.v_cache = reinterpret_cast<const uint8_t*>(p.v_cache);
-  a.k_scales = k_scales;
-  a.v_scales = v_scales;
+  a.k_scales = k_scales, a.v_scales = v_scales;
   a.block_table = p.block_table;
   a.seq_lens = p.seq_lens;
-  a.o = p.o;
-  a.lse = p.lse;
+  a.o = p.o, a.lse = p.lse;
   a.o_f32 = p.o_dtype == ATTN_DTYPE_F32;
-  const size_t rows = (size_t)p.batch * p.num_q_heads;
-  if (plan.max_splits > 1) {
-    a.part_o = reinterpret_cast<float*>(workspace);
-    a.part_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) +
-                                          (plan.max_splits * rows * p.head_dim * sizeof(float) + 255) / 256 * 256);
-  }
-  a.batch = p.batch;
-  a.hq = p.num_q_heads;
-  a.hkv = p.num_kv_heads;
-  a.group = p.num_q_heads / p.num_kv_heads;
-  a.max_blocks = p.max_blocks_per_seq;
-  a.num_blocks = p.num_blocks;
-  a.split_tokens = plan.split_tokens;
+  a.q_bs = a.o_bs = (long long)p.num_q_heads * p.head_dim;
+  a.q_hs = a.o_hs = p.head_dim;
+  a.lse_bs = p.num_q_heads, a.lse_hs = 1;
+  a.batch = p.batch, a.max_q = 1;
+  a.hkv = p.num_kv_heads, a.group = p.num_q_heads / p.num_kv_heads;
+  a.max_blocks = p.max_blocks_per_seq, a.num_blocks = p.num_blocks;
+  const int cap = p.max_blocks_per_seq * BS;
+  a.max_len = p.max_seq_len > 0 && p.max_seq_len < cap ? p.max_seq_len : cap;
   a.scale_log2 = p.scale * LOG2E;
   a.error_flags = p.error_flags;
   a.planted = planted_bounds_site();
-  const bool wide = a.group > 8;
-  if (p.head_dim == 128)
-    return wide ? launch<128, 2>(a, plan.max_splits, stream) : launch<128, 1>(a, plan.max_splits, stream);
-  return wide ? launch<64, 2>(a, plan.max_splits, stream) : launch<64, 1>(a, plan.max_splits, stream);
+  return a;
+}
+
+// A chunk's tiles; max_q rows at most per sequence.
+static Args chunk_args(const attn_prefill_params& p, const uint8_t* k_scales, const uint8_t* v_scales) {
+  Args a;
+  memset(&a, 0, sizeof(a));
+  a.q = reinterpret_cast<const __nv_bfloat16*>(p.q);
+  a.k_cache = reinterpret_cast<const uint8_t*>(p.k_cache);
+  a.v_cache = reinterpret_cast<const uint8_t*>(p.v_cache);
+  a.k_scales = k_scales, a.v_scales = v_scales;
+  a.block_table = p.block_table;
+  a.seq_lens = p.seqlens_k;
+  a.cu_q = p.cu_seqlens_q, a.q_lens = p.seqlens_q;
+  a.o = p.o, a.lse = p.lse;
+  a.o_f32 = p.o_dtype == ATTN_DTYPE_F32;
+  a.q_bs = p.q_batch_stride, a.q_hs = p.q_head_stride, a.q_rs = p.q_row_stride;
+  a.o_bs = p.o_batch_stride, a.o_hs = p.o_head_stride, a.o_rs = p.o_row_stride;
+  a.lse_hs = p.cu_seqlens_q ? p.total_q : p.seqlen_q, a.lse_bs = (long long)p.num_q_heads * p.seqlen_q;
+  a.causal = p.causal ? 1 : 0;
+  a.batch = p.batch, a.max_q = p.seqlen_q, a.total_q = p.cu_seqlens_q ? p.total_q : 0;
+  a.hkv = p.num_kv_heads, a.group = p.num_q_heads / p.num_kv_heads;
+  a.max_blocks = p.max_blocks_per_seq, a.num_blocks = p.num_blocks;
+  const int cap = p.max_blocks_per_seq * BS;
+  a.max_len = p.seqlen_k < cap ? p.seqlen_k : cap;
+  a.scale_log2 = p.scale * LOG2E;
+  a.error_flags = p.error_flags;
+  a.planted = planted_bounds_site();
+  return a;
+}
+
+}  // namespace bsdecode
+
+bool prefill_has_few_rows(const attn_prefill_params& p) {
+  using namespace bsdecode;
+  const long long tiles = ((long long)p.seqlen_q * (p.num_q_heads / p.num_kv_heads) + 15) / 16;
+  if (p.batch * tiles > 65535 || p.num_kv_heads > 65535) return false;
+  // Estimates of both sides in ns, from the bounds of the lengths, fitted to
+  // measurements (chunk, context, query / kv heads, head_dim; this side against
+  // the other): 1, 6000, 8/1, 128: 10 against 28 us; 3 x 22, 3000, 16/4, 128: 16
+  // against 28; 4 x 16, 6000, 32/8, 128: 47 against 67; 4 x 100, 500, 32/8, 128: 37
+  // against 28; 5 x 300, 3000, 16/4, 128: 152 against 53.
+  const int cap = p.max_blocks_per_seq * BS, len = p.seqlen_k < cap ? p.seqlen_k : cap;
+  const double blocks = (len + BS - 1) / BS, wide = p.head_dim / 128.0;
+  const double few = 4000 + p.batch * tiles * (double)p.num_kv_heads * blocks * (p.head_dim == 128 ? 1.1 : 0.45);
+  const double dense = (len > 512 ? 20000 : 9000) + p.batch * (double)p.num_kv_heads * len * wide * 0.154 +
+                       p.batch * (double)((p.seqlen_q + 127) / 128) * p.num_q_heads / 2 * ((len + 127) / 128) * 15 * wide;
+  return few < dense;
+}
+
+size_t prefill_few_rows_workspace_bytes(const attn_prefill_params& p) {
+  size_t bytes = 0;
+  bsdecode::dispatch(bsdecode::chunk_args(p, nullptr, nullptr), p.head_dim, 0, nullptr, &bytes, nullptr);
+  return bytes;
+}
+
+attn_status_t launch_prefill_few_rows(const attn_prefill_params& p, const uint8_t* k_scales, const uint8_t* v_scales,
+                                      void* workspace, cudaStream_t stream) {
+  return bsdecode::dispatch(bsdecode::chunk_args(p, k_scales, v_scales), p.head_dim, 0, workspace, nullptr, stream);
+}
+
+size_t decode_block_scaled_workspace_bytes(const attn_decode_params& p) {
+  size_t bytes = 0;
+  if (p.batch > 0) bsdecode::dispatch(bsdecode::decode_args(p, nullptr, nullptr), p.head_dim, p.num_splits, nullptr, &bytes, nullptr);
+  return bytes;
+}
+
+attn_status_t launch_decode_block_scaled(const attn_decode_params& p, const uint8_t* k_scales, const uint8_t* v_scales,
+                                         void* workspace, cudaStream_t stream) {
+  return bsdecode::dispatch(bsdecode::decode_args(p, k_scales, v_scales), p.head_dim, p.num_splits, workspace, nullptr, stream);
 }
 
 }  // namespace attn

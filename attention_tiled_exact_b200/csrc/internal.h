@@ -138,9 +138,14 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream);
 attn_status_t launch_gather(const attn_gather_params& p, int zero_to, bool flag_width, cudaStream_t stream);
 
 // Attention over the block-scaled 8-bit cache (decode and chunked prefill).
-DecodePlan plan_decode_block_scaled(const attn_decode_params& p);
+size_t decode_block_scaled_workspace_bytes(const attn_decode_params& p);
 attn_status_t launch_decode_block_scaled(const attn_decode_params& p, const uint8_t* k_scales, const uint8_t* v_scales,
-                                         const DecodePlan& plan, void* workspace, cudaStream_t stream);
+                                         void* workspace, cudaStream_t stream);
+// Chunks of few rows by the decode kernel (prefill_has_few_rows tells which).
+bool prefill_has_few_rows(const attn_prefill_params& p);
+size_t prefill_few_rows_workspace_bytes(const attn_prefill_params& p);
+attn_status_t launch_prefill_few_rows(const attn_prefill_params& p, const uint8_t* k_scales, const uint8_t* v_scales,
+                                      void* workspace, cudaStream_t stream);
 size_t prefill_block_scaled_workspace_bytes(const attn_prefill_params& p);
 attn_status_t launch_prefill_block_scaled(const attn_prefill_params& p, const uint8_t* k_scales,
                                           const uint8_t* v_scales, void* workspace, cudaStream_t stream);

@@ -1,5 +1,6 @@
-// Prefill over the block-scaled 8-bit cache (attn_prefill_paged_block_scaled):
-// the pages' values are written to the workspace as dense bf16 (code * 2^e has
+// Prefill over the block-scaled 8-bit cache (attn_prefill_paged_block_scaled).
+// Chunks of few rows go to the decode kernel, which reads the codes themselves
+// (prefill_has_few_rows). For the others the pages' values are written to the workspace as dense bf16 (code * 2^e has
 // 4 significant bits, so that is exact) and the dense prefill kernel attends to
 // them. The first step moves 5 bytes per cached element and kv head once; the
 // second one is bound by the tensor core, so for chunks of many rows the first
@@ -39,11 +40,14 @@ static attn_prefill_params dense_params(const attn_prefill_params& p, uint8_t* k
 }
 
 size_t prefill_block_scaled_workspace_bytes(const attn_prefill_params& p) {
+  if (p.batch == 0 || p.seqlen_q == 0) return 0;
+  if (prefill_has_few_rows(p)) return prefill_few_rows_workspace_bytes(p);
   return 2 * dense_bytes(p) + prefill_split_workspace_bytes(dense_params(p, nullptr));
 }
 
 attn_status_t launch_prefill_block_scaled(const attn_prefill_params& p, const uint8_t* k_scales,
                                           const uint8_t* v_scales, void* workspace, cudaStream_t stream) {
+  if (prefill_has_few_rows(p)) return launch_prefill_few_rows(p, k_scales, v_scales, workspace, stream);
   const int width = dense_width(p);
   uint8_t* k = reinterpret_cast<uint8_t*>(workspace);
   uint8_t* v = k + dense_bytes(p);

@@ -712,8 +712,11 @@ ATTN_API attn_status_t attn_gather_paged(const attn_gather_params* p, attn_strea
  * attn_decode_paged over the block-scaled 8-bit cache: p as there with
  * kv_dtype == ATTN_DTYPE_FP8_E4M3 (k_scale / v_scale are ignored), head_dim 64
  * or 128 and any num_q_heads / num_kv_heads from 1 to 16. Same workspace
- * protocol; the size depends on the device's SM count. Scales of the blocks of
- * one sequence and head may differ by up to 2^100.
+ * protocol; the size depends on the device's SM count. Each sequence is cut by
+ * its own length: into as many splits as the call finds best (num_splits == 0),
+ * not at all (1), or into num_splits rounded down to a power of two up to 8 or
+ * to a multiple of 8 (fewer where they would be shorter than 128 tokens).
+ * Scales of the blocks of one sequence and head may differ by up to 2^100.
  */
 ATTN_API attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* p, const uint8_t* k_scales,
                                                       const uint8_t* v_scales, void* workspace,

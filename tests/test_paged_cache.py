@@ -399,9 +399,9 @@ def _decode_run(lib, c, **kw):
 @gpu
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G", [1, 3, 4, 8, 9, 16])
-@pytest.mark.parametrize("num_splits", [0, 1, 5])
+@pytest.mark.parametrize("num_splits", [0, 1, 5, 16])
 def test_decode_block_scaled_matches_definition(lib, D, G, num_splits):
-    c = _decode_case([1, 0, 15, 16, 17, 100, 643, 1500], 2 * G, 2, D, 100 + G)
+    c = _decode_case([1, 0, 15, 16, 17, 100, 643, 2500], 2 * G, 2, D, 100 + G)
     o, lse, tol, ltol = _decode_want(c)
     for dtype in (torch.float32, torch.bfloat16):
         go, gl, flags = _decode_run(lib, c, num_splits=num_splits, out_dtype=dtype, max_seq_len=max(c["lens"]))
@@ -421,7 +421,7 @@ def test_decode_block_scaled_far_scales(lib, spread):
     shift = ((torch.rand(c["vs"].shape, generator=g) * 2 - 1) * spread).round().to(torch.int32)
     c["vs"] = torch.where(live, c["vs"].int() + shift, 255).to(torch.uint8)
     o, lse, tol, ltol = _decode_want(c)
-    for n in (1, 0, 7):
+    for n in (1, 0, 7, 16):
         go, gl, flags = _decode_run(lib, c, num_splits=n, out_dtype=torch.float32)
         assert flags == 0
         _within(go, o, tol + 2.0 ** -21 * o.abs(), f"O splits {n}")
@@ -448,7 +448,7 @@ def test_decode_block_scaled_nan_in_live_tokens(lib):
     c["kc"][int(c["table"][0, 1]), 0, 3, 5] = 0x7F
     c["vs"][int(c["table"][1, 0]), 1] = 255
     c["vc"][int(c["table"][3, 30]), 1, 3, 9] = 0xFF
-    for splits in (1, 3):
+    for splits in (1, 3, 0):
         o, lse, _ = _decode_run(lib, c, num_splits=splits)
         o, lse = o.cpu(), lse.cpu()
         assert torch.isnan(o[0, :2]).all() and torch.isnan(lse[0, :2]).all() and torch.isfinite(o[0, 2:]).all()
