@@ -1,15 +1,16 @@
 // Writing the paged cache (attn_append_paged) and reading it back
 // (attn_gather_paged), for sm_100a.
 //
-// Append, one launch with two kinds of blocks. The first blocks turn the query
-// rows (turn_rows). In the others a warp owns one kv head of K or of V and a
-// window of rows: it finds the runs of consecutive slots that start in the
-// window, and handles a run (at most 16 tokens, one cache block) as a whole.
-// A lane holds one 16-element unit of 16 * units / 32 of the block's tokens in
-// registers: kept tokens (in front of the run) are read back as values, new
-// ones are read and turned; one warp reduction gives the block's largest
-// magnitude and with it the scale, and the codes go out. So a block's scale
-// and codes come from one warp, without atomics, whatever the grid's order.
+// Append, one launch with two kinds of CTAs. The first ones turn the query rows
+// (turn_rows). The others own a window of rows and a few kv heads: they find the
+// runs of consecutive slots that start in the window, compute the angles of the
+// runs' rows once for all heads, and two warps handle a run (at most 16 tokens,
+// one cache block) of one head of K or V as a whole. A lane holds one 16-element
+// unit of 16 * units / 64 of the block's tokens in registers: kept tokens (in
+// front of the run) are read back as values, new ones are read and turned; one
+// reduction gives the block's largest magnitude and with it the scale, and the
+// codes go out. So a block's scale and codes come from one pair of warps,
+// without atomics, whatever the grid's order.
 //   value -> code: e = smallest integer with amax <= 448 * 2^e,
 //   code = e4m3(x * 2^-e), the only rounding of a key or value; it is made
 //   from the fp32 turned key, not from a bf16 copy of it.
@@ -31,7 +32,7 @@
 namespace attn {
 namespace cache {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = rotary::THREADS;
 constexpr int WARPS = THREADS / 32;
 constexpr int BS = 16;
 constexpr unsigned FULL = 0xffffffffu;
@@ -51,37 +52,75 @@ struct Append {
   const int32_t* positions;
   int32_t* flags;
   int total, hkv, num_slots;
-  int window;  // rows whose runs one warp handles: 1 or 16
+  int window;      // rows whose runs one CTA handles: 1 or 16
+  int heads_per;   // kv heads of a CTA
+  int head_chunks; // CTAs that share a window's heads
 };
 
+constexpr int PAIRS = WARPS / 2;       // pairs of warps, each with its own run
+constexpr int SPAN = 31;               // rows that the runs of a window may reach over
+
+constexpr int KV_STAGES = 2;           // runs whose rows are on their way
+constexpr int KV_SLOTS = 4;            // 16-byte vectors of a thread and run: 32 elements
+
+struct __align__(16) AppendSmem {
+  uint4 ring[KV_STAGES][KV_SLOTS][THREADS];  // each thread's own
+  float2 turn[SPAN][rotary::MAX_PAIRS];  // magnitude * (cos, sin) of the window's rows
+  float amax[2][PAIRS][2];
+};
+
+// A lane's part of a run: unit u of the tokens grp + GROUPS * i of the block.
+template <int D>
+struct Lanes {
+  static constexpr int UNITS = D / 16, GROUPS = 64 / UNITS, PER = BS / GROUPS;
+  int u, grp;
+  __device__ __forceinline__ Lanes() : u(lane_id() % UNITS), grp(lane_id() / UNITS + (warp_id() & 1) * (GROUPS / 2)) {}
+};
+
+// Starts the copies of the lane's rows of a run (as in write_run) to its slots of a stage.
+template <int D, bool INTER>
+__device__ __forceinline__ void fetch_run(const __nv_bfloat16* x, long long rs, int rotary_dim, int t, int n, int off0,
+                                          uint4 (*stage)[THREADS]) {
+  using L = Lanes<D>;
+  const L l;
+  const int2 off = rotary::unit_offsets<INTER>(l.u, rotary_dim);
+#pragma unroll
+  for (int i = 0; i < L::PER; ++i) {
+    const int o = l.grp + L::GROUPS * i;
+    if (o < off0 || o >= off0 + n) continue;
+    const __nv_bfloat16* src = x + (long long)(t + o - off0) * rs;
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(&stage[2 * i + v][threadIdx.x])),
+                   "l"(src + (v ? off.y : off.x))
+                   : "memory");
+  }
+}
+
 // One run of `n` tokens from row `t` on, to offsets off0 .. off0 + n - 1 of a
-// block whose codes (or bf16 elements) of this head start at `page`.
+// block whose codes (or bf16 elements) of this head start at `page`, by a pair
+// of warps. turn: the angles of the first row, or NULL. amax_at: alternates from
+// run to run.
 template <int D, bool FP8, bool INTER>
-__device__ __forceinline__ void write_run(const Append& a, const __nv_bfloat16* x, long long rs, bool turn_rows,
-                                          int t, int n, int off0, uint8_t* page, uint8_t* scale) {
-  constexpr int UNITS = D / 16, GROUPS = 32 / UNITS, PER = BS / GROUPS;
-  const int lane = lane_id();
-  const int u = lane % UNITS, grp = lane / UNITS;
-  const int rotary_dim = turn_rows ? a.turn.rotary_dim : 0;
-  const bool turned = u * 16 < rotary_dim;
-  const int2 off = rotary::unit_offsets<INTER>(u, rotary_dim);
-  const float old_scale = FP8 && off0 > 0 ? bscale::scale_of(*scale) : 0.f;
+__device__ __forceinline__ void write_run(const uint4 (*stage)[THREADS],
+                                          const float2 (*turn)[rotary::MAX_PAIRS], int rotary_dim, int n, int off0, uint8_t* page, uint8_t* scale,
+                                          float (*amax_at)[2]) {
+  using L = Lanes<D>;
+  constexpr int GROUPS = L::GROUPS, PER = L::PER;
+  const L l;
+  const int lane = lane_id(), pair = warp_id() / 2, half = warp_id() & 1, u = l.u, grp = l.grp;
+  const bool turned = turn && u * 16 < rotary_dim;
+  const int2 off = rotary::unit_offsets<INTER>(u, turn ? rotary_dim : 0);
   const int old_byte = FP8 && off0 > 0 ? *scale : -1;
+  const float old_scale = old_byte >= 0 ? bscale::scale_of(old_byte) : 0.f;
   float val[PER][16];
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int o = grp + GROUPS * i;  // this lane's token of the block
     if (o >= off0 && o < off0 + n) {
-      const long long row = t + (o - off0);
-      const __nv_bfloat16* src = x + row * rs;
-      rotary::load8(src + off.x, &val[i][0]);
-      rotary::load8(src + off.y, &val[i][8]);
-      if (turned) {
-        float c[8], s[8];
-        rotary::unit_turn(a.turn, __ldg(a.positions + row), u, c, s);
-        rotary::turn16<INTER>(val[i], c, s);
-      }
+      rotary::load8(reinterpret_cast<const __nv_bfloat16*>(&stage[2 * i][threadIdx.x]), &val[i][0]);
+      rotary::load8(reinterpret_cast<const __nv_bfloat16*>(&stage[2 * i + 1][threadIdx.x]), &val[i][8]);
     } else if (FP8 && o < off0) {
       bscale::load_codes8(page + o * D + off.x, &val[i][0]);
       bscale::load_codes8(page + o * D + off.y, &val[i][8]);
@@ -91,17 +130,38 @@ __device__ __forceinline__ void write_run(const Append& a, const __nv_bfloat16* 
 #pragma unroll
       for (int j = 0; j < 16; ++j) val[i][j] = 0.f;
     }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int o = grp + GROUPS * i;
+    if (turned && o >= off0 && o < off0 + n) {
+      float c[8], s[8];
+      rotary::unit_turn(turn[o - off0], u, c, s);
+      rotary::UnitTurn ut;
+      ut.set(c, s);
+      rotary::turn16<INTER>(val[i], ut);
+    }
     if constexpr (FP8) {
 #pragma unroll
+      for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(val[i][j]));  // passes over a NaN
+    }
+  }
+  if (FP8 && amax == INFINITY) {  // an infinity is stored as NaN, and is outside the maximum
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
       for (int j = 0; j < 16; ++j) {
-        if (!(fabsf(val[i][j]) < INFINITY)) val[i][j] = NAN;  // stored as NaN, and outside the maximum
+        if (fabsf(val[i][j]) == INFINITY) val[i][j] = NAN;
         amax = fmaxf(amax, fabsf(val[i][j]));
       }
-    }
   }
   if constexpr (FP8) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, d));
+    if (lane == 0) amax_at[pair][half] = amax;
+    named_bar_sync(1 + pair, 64);  // both warps have read the old scale, too
+    amax = fmaxf(amax_at[pair][0], amax_at[pair][1]);
     const int e = bscale::exponent_for(amax);
     const float mul = bscale::pow2i(-e);
     const bool recode = e + bscale::BIAS != old_byte;
@@ -113,7 +173,7 @@ __device__ __forceinline__ void write_run(const Append& a, const __nv_bfloat16* 
         bscale::store_codes8(page + o * D + off.y, &val[i][8], mul);
       }
     }
-    if (lane == 0) *scale = (uint8_t)(e + bscale::BIAS);
+    if (lane == 0 && half == 0) *scale = (uint8_t)(e + bscale::BIAS);
   } else {
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(page);
 #pragma unroll
@@ -128,18 +188,18 @@ __device__ __forceinline__ void write_run(const Append& a, const __nv_bfloat16* 
 }
 
 template <int D, bool FP8, bool INTER>
-__global__ void __launch_bounds__(THREADS) append_kernel(const Append a) {
+__global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
+  extern __shared__ __align__(16) uint8_t smem[];
   if ((int)blockIdx.x < a.q_blocks) {
-    rotary::turn_rows<__nv_bfloat16, __nv_bfloat16, INTER>(a.rows, a.turn,
-                                                           (long long)blockIdx.x * THREADS + threadIdx.x);
+    const int group = blockIdx.x / a.rows.tiles;
+    rotary::turn_rows<__nv_bfloat16, __nv_bfloat16, INTER, D, true>(a.rows, a.turn, blockIdx.x - group * a.rows.tiles,
+                                                                    group, smem);
     return;
   }
+  AppendSmem& sm = *reinterpret_cast<AppendSmem*>(smem);
   const int lane = lane_id();
-  const long long item = (long long)(blockIdx.x - a.q_blocks) * WARPS + warp_id();
-  const bool is_v = item & 1;
-  const int h = (int)((item >> 1) % a.hkv);
-  const long long first = (item >> 1) / a.hkv * a.window;  // the window's first row
-  if (first >= a.total) return;
+  const int item = blockIdx.x - a.q_blocks, chunk = item % a.head_chunks;
+  const long long first = (long long)(item / a.head_chunks) * a.window;  // the window's first row
   // Lane i holds the slot of row first - 1 + i: the window's rows, the one in
   // front of it and the 15 that a run may reach into behind it.
   const long long row = first - 1 + lane;
@@ -147,21 +207,68 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const Append a) {
   const int before = __shfl_up_sync(FULL, slot, 1);
   const bool good = slot >= 0 && slot < a.num_slots;
   const bool mine = lane >= 1 && lane <= a.window && row < a.total;
-  if (mine && slot >= a.num_slots && a.flags) atomicOr(a.flags, ATTN_FAULT_BAD_BLOCK);
+  if (mine && slot >= a.num_slots && a.flags && chunk == 0 && threadIdx.x < 32)
+    atomicOr(a.flags, ATTN_FAULT_BAD_BLOCK);
   const bool follows = lane >= 1 && good && (slot & (BS - 1)) != 0 && before == slot - 1;
   const unsigned runs = __ballot_sync(FULL, mine && good && !follows), rest = __ballot_sync(FULL, follows);
-  const __nv_bfloat16* x = is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs;
-  const long long rs = is_v ? a.v_rs : a.k_rs;
-  uint8_t* pool = is_v ? a.v_cache : a.k_cache;
-  uint8_t* scales = is_v ? a.v_scales : a.k_scales;
-  for (unsigned left = runs; left; left &= left - 1) {
-    const int i = __ffs(left) - 1;
-    const int n = i == 31 ? 1 : 1 + __ffs(~(rest >> (i + 1))) - 1;  // rows that follow row i, and it
-    const int at = __shfl_sync(FULL, slot, i);
-    const long long blk = (long long)(at / BS) * a.hkv + h;
-    write_run<D, FP8, INTER>(a, x, rs, !is_v, (int)(first - 1 + i), n, at % BS, pool + blk * (BS * D * (FP8 ? 1 : 2)),
-                             FP8 ? scales + blk : nullptr);
+  if (runs == 0) return;
+  // The pair's runs: item by item (kv head, K or V), and in each the window's runs.
+  const int h0 = chunk * a.heads_per, items = 2 * (min(a.hkv, h0 + a.heads_per) - h0);
+  const int rotary_dim = a.turn.rotary_dim;
+  struct Cursor {
+    int it;
+    unsigned left;
+  };
+  auto advance = [&](Cursor& c) {
+    c.left &= c.left - 1;
+    if (c.left == 0) c.it += PAIRS, c.left = runs;
+  };
+  // First lane of the cursor's run and its length.
+  auto run_of = [&](const Cursor& c, int& i, int& n) {
+    i = __ffs(c.left) - 1;
+    n = i == 31 ? 1 : 1 + __ffs(~(rest >> (i + 1))) - 1;  // rows that follow row i, and it
+  };
+  auto fetch = [&](const Cursor& c, int stage) {
+    if (c.it < items) {
+      int i, n;
+      run_of(c, i, n);
+      const int off0 = __shfl_sync(FULL, slot, i) % BS, h = h0 + (c.it >> 1);
+      const bool is_v = c.it & 1;
+      fetch_run<D, INTER>(is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs, is_v ? a.v_rs : a.k_rs, is_v ? 0 : rotary_dim,
+                          (int)(first - 1 + i), n, off0, sm.ring[stage]);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Cursor now = {warp_id() / 2, runs}, next = now;
+  int stage = 0;
+  fetch(next, 0);
+  const int pairs = rotary_dim / 2;
+  if (pairs > 0) {
+    // The rows of the runs: from a run's first row to the last that follows it.
+    unsigned rows = runs;
+    for (int i = 0; i < BS - 1; ++i) rows |= (rows << 1) & rest;
+    const int p = threadIdx.x % rotary::MAX_PAIRS;
+    if (p < pairs)
+      for (int r = threadIdx.x / rotary::MAX_PAIRS; r < SPAN; r += THREADS / rotary::MAX_PAIRS)
+        if (rows >> (r + 1) & 1) sm.turn[r][p] = rotary::pair_turn(a.turn, __ldg(a.positions + first + r), p);
+    __syncthreads();
   }
+  while (now.it < items) {
+    advance(next);
+    fetch(next, stage ^ 1);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    int i, n;
+    run_of(now, i, n);
+    const bool is_v = now.it & 1;
+    const int h = h0 + (now.it >> 1), at = __shfl_sync(FULL, slot, i);
+    const long long blk = (long long)(at / BS) * a.hkv + h;
+    write_run<D, FP8, INTER>(sm.ring[stage], !is_v && pairs > 0 ? sm.turn + (i - 1) : nullptr, rotary_dim, n, at % BS,
+                             (is_v ? a.v_cache : a.k_cache) + blk * (BS * D * (FP8 ? 1 : 2)),
+                             FP8 ? (is_v ? a.v_scales : a.k_scales) + blk : nullptr, sm.amax[stage]);
+    now = next;
+    stage ^= 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 struct Gather {
@@ -245,13 +352,28 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const Gather g, long lo
 
 }  // namespace cache
 
+template <int D, bool FP8, bool INTER>
+static attn_status_t launch_append_kernel(const cache::Append& a, unsigned blocks, cudaStream_t stream) {
+  // The query CTAs' ring, if there are any.
+  constexpr int RING = rotary::ring_bytes<__nv_bfloat16>(), OWN = (int)sizeof(cache::AppendSmem), SMEM = RING > OWN ? RING : OWN;
+  auto kern = cache::append_kernel<D, FP8, INTER>;
+  static DeviceOnce setup;
+  const attn_status_t st = setup.run([&]() -> attn_status_t {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
+      cudaGetLastError();
+      return ATTN_ERR_CUDA;
+    }
+    return ATTN_OK;
+  });
+  if (st != ATTN_OK) return st;
+  kern<<<blocks, cache::THREADS, a.q_blocks ? SMEM : OWN, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 template <int D, bool FP8>
 static attn_status_t launch_append_d(const cache::Append& a, bool inter, unsigned blocks, cudaStream_t stream) {
-  if (inter)
-    cache::append_kernel<D, FP8, true><<<blocks, cache::THREADS, 0, stream>>>(a);
-  else
-    cache::append_kernel<D, FP8, false><<<blocks, cache::THREADS, 0, stream>>>(a);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  return inter ? launch_append_kernel<D, FP8, true>(a, blocks, stream)
+               : launch_append_kernel<D, FP8, false>(a, blocks, stream);
 }
 
 attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
@@ -283,20 +405,24 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
     r.slots = p.slot_map;
     r.tokens = p.total, r.seqlen = p.total;
     r.hq = r.heads = p.num_q_heads;
-    r.units = p.head_dim / 16;
-    r.head_groups = rotary::head_groups_for(r.tokens, r.heads, r.units, sms);
     r.q_hs = p.q_head_stride, r.q_rs = p.q_row_stride;
     r.qo_hs = p.qo_head_stride, r.qo_rs = p.qo_row_stride;
-    const long long threads = r.tokens * r.head_groups * r.units;
-    const long long q_blocks = (threads + cache::THREADS - 1) / cache::THREADS;
+    rotary::plan_rows(r, p.head_dim, true, sms);
+    const long long q_blocks = (long long)r.tiles * r.head_groups;
     if (q_blocks > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
     a.q_blocks = (int)q_blocks;
   }
-  // A warp per row while that does not fill the machine (a decode step has one
-  // run per row), a warp per 16 rows beyond (a chunk has one run per 16).
-  a.window = 2LL * p.num_kv_heads * p.total <= 32LL * sms ? 1 : 16;
-  const long long items = 2LL * p.num_kv_heads * ((p.total + a.window - 1) / a.window);
-  const long long blocks = a.q_blocks + (items + cache::WARPS - 1) / cache::WARPS;
+  // A CTA per row while that does not fill the machine (a decode step has one
+  // run per row), per 16 rows beyond (a chunk has one run per 16); a window's
+  // heads go to as many CTAs as run at once, a head each for a pair of warps at
+  // the least.
+  a.window = p.total <= 2 * sms ? 1 : 16;
+  const long long windows = (p.total + a.window - 1) / a.window;
+  const int most = (p.num_kv_heads + 1) / 2;  // two heads: a head of K or V for each pair
+  const long long chunks = 4LL * sms / windows;
+  a.heads_per = (int)(chunks >= most ? 2 : chunks > 1 ? (p.num_kv_heads + chunks - 1) / chunks : p.num_kv_heads);
+  a.head_chunks = (p.num_kv_heads + a.heads_per - 1) / a.heads_per;
+  const long long blocks = a.q_blocks + windows * a.head_chunks;
   if (blocks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   const bool fp8 = p.kv_dtype == ATTN_DTYPE_FP8_E4M3, inter = p.interleaved != 0;
   if (p.head_dim == 128)

@@ -30,67 +30,64 @@ __device__ __forceinline__ int2 unit_offsets(int u, int rotary_dim) {
   return make_int2(16 * u, 16 * u + 8);
 }
 
-// magnitude * (cos, sin) of position * inv_freq for the pairs of unit u. The
-// angle is reduced to half turns in fp64 (an fp32 product is off by half a
-// step of the angle, 0.03 rad at position 10^6) and only the remainder, in
-// [-1, 1], goes to fp32.
-__device__ __forceinline__ void unit_turn(const Turn& t, int position, int u, float (&c)[8], float (&s)[8]) {
+// magnitude * (cos, sin) of position * inv_freq[pair]. The angle is reduced to
+// half turns in fp64 (an fp32 product is off by half a step of the angle, 0.03
+// rad at position 10^6) and only the remainder, in [-1, 1], goes to fp32.
+__device__ __forceinline__ float2 pair_turn(const Turn& t, int position, int pair) {
   constexpr double INV_PI = 0.31830988618379067154;
+  double h = (double)position * (__ldg(t.inv_freq + pair) * INV_PI);
+  h -= 2.0 * rint(0.5 * h);
+  float si, co;
+  sincospif((float)h, &si, &co);
+  return make_float2(co * t.magnitude, si * t.magnitude * t.sign);
+}
+
+constexpr int MAX_PAIRS = 64;
+
+// The angles of unit u out of a row of them.
+__device__ __forceinline__ void unit_turn(const float2* row, int u, float (&c)[8], float (&s)[8]) {
+  const float4* cs = reinterpret_cast<const float4*>(row + 8 * u);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    double h = (double)position * (__ldg(t.inv_freq + 8 * u + i) * INV_PI);
-    h -= 2.0 * rint(0.5 * h);
-    float si, co;
-    sincospif((float)h, &si, &co);
-    c[i] = co * t.magnitude;
-    s[i] = si * t.magnitude * t.sign;
+  for (int j = 0; j < 4; ++j) {
+    const float4 y = cs[j];
+    c[2 * j] = y.x, s[2 * j] = y.y, c[2 * j + 1] = y.z, s[2 * j + 1] = y.w;
   }
 }
 
-template <bool INTER>
-__device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int a = INTER ? 2 * i : i, b = INTER ? 2 * i + 1 : i + 8;
-    const float x1 = x[a], x2 = x[b];
-    x[a] = x1 * c[i] - x2 * s[i];
-    x[b] = x2 * c[i] + x1 * s[i];
-  }
-}
-
-// Eight row elements as they lie in memory, and as fp32.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float* x) const {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+// magnitude * (cos, sin, -sin) of a unit's 8 pairs, two pairs per register pair
+// (the packed fp32 instructions take two at a time).
+struct UnitTurn {
+  float2 c[4], s[4], ns[4];
+  __device__ __forceinline__ void set(const float (&co)[8], const float (&si)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      c[i] = make_float2(co[2 * i], co[2 * i + 1]);
+      s[i] = make_float2(si[2 * i], si[2 * i + 1]);
+      ns[i] = make_float2(-si[2 * i], -si[2 * i + 1]);
     }
   }
 };
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const float4*>(p);
-    b = *reinterpret_cast<const float4*>(p + 4);
+
+template <bool INTER>
+__device__ __forceinline__ void turn16(float (&x)[16], const UnitTurn& t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int a = INTER ? 4 * i : 2 * i, b = INTER ? 4 * i + 1 : 2 * i + 8, d = INTER ? 2 : 1;
+    const float2 x1 = make_float2(x[a], x[a + d]), x2 = make_float2(x[b], x[b + d]);
+    const float2 y1 = __ffma2_rn(x2, t.ns[i], __fmul2_rn(x1, t.c[i]));
+    const float2 y2 = __ffma2_rn(x1, t.s[i], __fmul2_rn(x2, t.c[i]));
+    x[a] = y1.x, x[a + d] = y1.y, x[b] = y2.x, x[b + d] = y2.y;
   }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
-};
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x) {
-  Raw8<T> r;
-  r.load(p);
-  r.get(x);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float* x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
@@ -109,85 +106,177 @@ struct Rows {
   void* k_out;
   const int32_t* positions;  // NULL: the row's index in its sequence
   const int32_t* slots;      // not NULL: rows with a negative slot are left alone, not those with a negative position
-  long long tokens;          // batch * seqlen
+  int tokens;                // batch * seqlen
   int seqlen, hq, heads;     // heads = hq + the heads of k
-  int units;                 // head_dim / 16
-  int head_groups;           // threads that share a token's heads
+  int head_groups;           // CTAs that share a tile's heads
+  int tiles;                 // token tiles of the CTAs
+  int by_heads;              // which of a warp's rows lie next to one another (below)
   long long q_bs, q_hs, q_rs, k_bs, k_hs, k_rs;
   long long qo_bs, qo_hs, qo_rs, ko_bs, ko_hs, ko_rs;
 };
 
-// Thread `index` of tokens * head_groups * units: unit index % units of one
-// token, for every head_groups-th head. Neighbouring lanes hold a row's units
-// (16-byte vectors, whole 128-byte lines for head_dim 128), then the next
-// token's. The rows of several heads are on their way while the angles are
-// computed, and the next ones while these are turned; they stay packed until
-// they are used, which keeps the kernel at 64 registers and 32 warps per SM.
-template <typename TI, typename TO, bool INTER>
-__device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, long long index) {
-  const int u = (int)(index % r.units);
-  const long long row = index / r.units;
-  const long long token = row % r.tokens;
-  const int group = (int)(row / r.tokens);
-  if (group >= r.head_groups) return;
-  const long long b = token / r.seqlen, pos_in_seq = token - b * r.seqlen;
-  const int position = r.positions ? __ldg(r.positions + token) : (int)pos_in_seq;
-  if (r.slots ? __ldg(r.slots + token) < 0 : position < 0) return;
+constexpr int THREADS = 256;
+constexpr int CTAS_PER_SM = 4;
+constexpr int STAGES = 4;  // rows of a thread that are on their way, and the one in use
+template <typename T>
+constexpr int ring_bytes() {
+  return STAGES * THREADS * 16 * (int)sizeof(T);
+}
+
+// A thread's own slots in shared memory: vector v of stage s of thread t at
+// (s * vectors + v) * THREADS + t, so that a warp's accesses are 512 bytes in a row.
+template <typename T>
+struct Ring {
+  static constexpr int VECS = 16 * (int)sizeof(T) / 16;  // 16-byte vectors of 16 elements
+  uint4* mine;
+  __device__ __forceinline__ explicit Ring(uint8_t* smem) : mine(reinterpret_cast<uint4*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ void fetch(int stage, const T* lo, const T* hi) {
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      const T* src = v < VECS / 2 ? lo + v * (16 / (int)sizeof(T)) : hi + (v - VECS / 2) * (16 / (int)sizeof(T));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(mine + (stage * VECS + v) * THREADS)),
+                   "l"(src)
+                   : "memory");
+    }
+  }
+  __device__ __forceinline__ void get(int stage, float* x) const {
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+      const uint4 r = mine[(stage * VECS + v) * THREADS];
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[8 * v + 2 * i] = __uint_as_float(w[i] << 16);
+          x[8 * v + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * v + i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+};
+
+// A tile of tokens, and of their heads every head_groups-th set from `group`. A
+// warp's lanes hold the units of a row (16-byte vectors, whole 128-byte lines
+// for head_dim 128), and of the rows that lie next to it in memory: the next
+// tokens' in [.., head, token, element], or (BY_HEADS) the next heads' in [token,
+// head, element], a set of them per step, which share their angles. The rows
+// come through a ring of cp.async stages in shared memory that belongs to the
+// thread alone; the first ones are fetched before the position is known. What
+// this costs is instructions as much as bytes: no division by a variable, the
+// loop unrolled over the ring, pointers that advance by addition, packed products.
+template <int D, bool BY_HEADS>
+struct Warp {
+  static constexpr int UNITS = D / 16, ROWS = 32 / UNITS;
+  static constexpr int HEADS = BY_HEADS ? ROWS : 1, TOKENS = ROWS / HEADS;
+  static constexpr int TILE = THREADS / 32 * TOKENS;
+};
+
+template <typename TI, typename TO, bool INTER, int D, bool BY_HEADS>
+__device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile, int group_index, uint8_t* smem) {
+  using W = Warp<D, BY_HEADS>;
+  const int lane = lane_id(), u = lane % W::UNITS, row = lane / W::UNITS, hsub = BY_HEADS ? row : 0;
+  const long long token_at = (long long)tile * W::TILE + warp_id() * W::TOKENS + (BY_HEADS ? 0 : row);
+  const bool live = token_at < r.tokens;
+  const int token = live ? (int)token_at : 0;
+  const int group = group_index * W::HEADS + hsub, step = r.head_groups * W::HEADS;
+  const int b = token / r.seqlen, pos_in_seq = token - b * r.seqlen;
   const bool turned = u * 16 < t.rotary_dim;
   const int2 off = unit_offsets<INTER>(u, t.rotary_dim);
   const TI* q = reinterpret_cast<const TI*>(r.q) + b * r.q_bs + pos_in_seq * r.q_rs;
   const TI* k = reinterpret_cast<const TI*>(r.k) + b * r.k_bs + pos_in_seq * r.k_rs;
-  TO* qo = reinterpret_cast<TO*>(r.q_out) + b * r.qo_bs + pos_in_seq * r.qo_rs;
-  TO* ko = reinterpret_cast<TO*>(r.k_out) + b * r.ko_bs + pos_in_seq * r.ko_rs;
-  constexpr int BATCH = sizeof(TI) == 2 ? 2 : 1;
-  Raw8<TI> raw[2][BATCH][2];
-  auto fetch = [&](int h0, Raw8<TI> (&to)[BATCH][2]) {
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int h = h0 + i * r.head_groups;
-      if (h < r.heads) {
-        const TI* src = h < r.hq ? q + h * r.q_hs : k + (h - r.hq) * r.k_hs;
-        to[i][0].load(src + off.x);
-        to[i][1].load(src + off.y);
+  Ring<TI> ring(smem);
+  // The next row to fetch: its head, counted on through q and k, and its address.
+  int fetch_h = live ? group : r.heads;
+  const TI* fetch_at = group < r.hq ? q + group * r.q_hs : k + (group - r.hq) * r.k_hs;
+  long long fetch_step = step * (group < r.hq ? r.q_hs : r.k_hs);
+  auto fetch = [&](int stage) {
+    if (fetch_h < r.heads) {
+      ring.fetch(stage, fetch_at + off.x, fetch_at + off.y);
+      const bool was_q = fetch_h < r.hq;
+      fetch_h += step;
+      fetch_at += fetch_step;
+      if (was_q && fetch_h >= r.hq) {
+        fetch_at = k + (fetch_h - r.hq) * r.k_hs;
+        fetch_step = step * r.k_hs;
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(group, raw[0]);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
+  const int position = !live ? -1 : r.positions ? __ldg(r.positions + token) : pos_in_seq;
+  const bool skipped = !live || (r.slots ? __ldg(r.slots + token) < 0 : position < 0);
   float c[8], s[8];
-  if (turned) unit_turn(t, position, u, c, s);
-  auto finish = [&](int h0, const Raw8<TI> (&from)[BATCH][2]) {
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int h = h0 + i * r.head_groups;
-      if (h < r.heads) {
-        float x[16];
-        from[i][0].get(x);
-        from[i][1].get(x + 8);
-        if (turned) turn16<INTER>(x, c, s);
-        TO* dst = h < r.hq ? qo + h * r.qo_hs : ko + (h - r.hq) * r.ko_hs;
-        store8(dst + off.x, x);
-        store8(dst + off.y, x + 8);
+  for (int i = 0; i < 8; ++i) c[i] = 1.f, s[i] = 0.f;
+  if constexpr (BY_HEADS) {  // the lanes of a unit compute PER of its angles each
+    constexpr int PER = 8 / W::HEADS;
+    float2 mine[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      mine[i] = turned && !skipped ? pair_turn(t, position, 8 * u + hsub * PER + i) : make_float2(1.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = __shfl_sync(0xffffffffu, mine[i % PER].x, i / PER * W::UNITS + u);
+      s[i] = __shfl_sync(0xffffffffu, mine[i % PER].y, i / PER * W::UNITS + u);
+    }
+  } else if (turned && !skipped) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 y = pair_turn(t, position, 8 * u + i);
+      c[i] = y.x, s[i] = y.y;
+    }
+  }
+  UnitTurn turn;
+  turn.set(c, s);
+  TO* ko = reinterpret_cast<TO*>(r.k_out) + b * r.ko_bs + pos_in_seq * r.ko_rs;
+  TO* to = group < r.hq ? reinterpret_cast<TO*>(r.q_out) + b * r.qo_bs + pos_in_seq * r.qo_rs + group * r.qo_hs
+                        : ko + (group - r.hq) * r.ko_hs;
+  long long to_step = step * (group < r.hq ? r.qo_hs : r.ko_hs);
+  int h = skipped ? r.heads : group;
+  while (h < r.heads) {
+#pragma unroll
+    for (int stage = 0; stage < STAGES; ++stage) {
+      if (h >= r.heads) break;
+      fetch((stage + STAGES - 1) % STAGES);
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      float x[16];
+      ring.get(stage, x);
+      if (turned) turn16<INTER>(x, turn);
+      store8(to + off.x, x);
+      store8(to + off.y, x + 8);
+      const bool was_q = h < r.hq;
+      h += step;
+      to += to_step;
+      if (was_q && h >= r.hq) {
+        to = ko + (h - r.hq) * r.ko_hs;
+        to_step = step * r.ko_hs;
       }
     }
-  };
-  const int step = BATCH * r.head_groups;
-  for (int h0 = group; h0 < r.heads; h0 += 2 * step) {
-    fetch(h0 + step, raw[1]);
-    finish(h0, raw[0]);
-    fetch(h0 + 2 * step, raw[0]);
-    finish(h0 + step, raw[1]);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// Threads that share a token's heads: one thread per head while the tokens
-// alone do not fill the machine, and fewer as they do, so that the angles of a
-// token are computed once for several heads.
-inline int head_groups_for(long long tokens, int heads, int units, int sm_count) {
-  const long long want = 2048LL * sm_count;  // threads: two rounds of 1024 per SM
-  long long g = tokens > 0 ? (want + tokens * units - 1) / (tokens * units) : 1;
-  const long long least = (heads + 15) / 16;  // at most 16 heads a thread
-  if (g < least) g = least;
-  return (int)(g > heads ? heads : g);
+// Token tiles, and the head groups for which the CTAs end soonest: rounds of
+// CTAs_PER_SM * SMs CTAs times what a CTA does, its steps and the angles (which
+// cost about as much as 4 steps). Queries and keys of 8192 tokens and 40 heads
+// of 128, by tokens: 2 groups (one round) 32 us, 1 group 34 us, 40 groups 65 us.
+inline void plan_rows(Rows& r, int head_dim, bool by_heads, int sm_count) {
+  const int rows = 32 / (head_dim / 16), warp_heads = by_heads ? rows : 1;
+  r.by_heads = by_heads ? 1 : 0;
+  const int tile_tokens = THREADS / 32 * (rows / warp_heads);
+  r.tiles = (int)(((long long)r.tokens + tile_tokens - 1) / tile_tokens);
+  const int sets = (r.heads + warp_heads - 1) / warp_heads;
+  const long long slots = (long long)CTAS_PER_SM * sm_count;
+  long long best = 0;
+  for (int g = 1; g <= sets; ++g) {
+    const long long rounds = (r.tiles * (long long)g + slots - 1) / slots;
+    const long long cost = rounds * ((sets + g - 1) / g * warp_heads + 4);
+    if (g == 1 || cost < best) best = cost, r.head_groups = g;
+  }
 }
 
 }  // namespace rotary
