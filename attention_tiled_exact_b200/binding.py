@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -188,14 +189,12 @@ def _load():
     lib.splitkv_lse_combine.argtypes = [_vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
                                         ctypes.c_int, _vp, _vp]
     lib.splitkv_lse_combine.restype = ctypes.c_int
-    for name, params in (("attn_rotary", RotaryParams), ("attn_plan_paged_step", PlanParams),
-                         ("attn_append_paged", AppendParams), ("attn_gather_paged", GatherParams)):
-        getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp]
+    # These take the parameters as packed bytes (see _packer) or by reference.
+    for name in ("attn_rotary", "attn_plan_paged_step", "attn_append_paged", "attn_gather_paged"):
+        getattr(lib, name).argtypes = [_vp, _vp]
         getattr(lib, name).restype = ctypes.c_int
-    for name, params in (("attn_decode_paged_block_scaled", DecodeParams),
-                         ("attn_prefill_paged_block_scaled", PrefillParams)):
-        getattr(lib, name).argtypes = [ctypes.POINTER(params), _vp, _vp, _vp, ctypes.c_size_t,
-                                       ctypes.POINTER(ctypes.c_size_t), _vp]
+    for name in ("attn_decode_paged_block_scaled", "attn_prefill_paged_block_scaled"):
+        getattr(lib, name).argtypes = [_vp, _vp, _vp, _vp, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t), _vp]
         getattr(lib, name).restype = ctypes.c_int
     lib.attn_status_string.argtypes = [ctypes.c_int]
     lib.attn_status_string.restype = ctypes.c_char_p
@@ -680,8 +679,19 @@ def decode_paged_noalloc(q, k_cache, v_cache, block_table, seq_lens, out, lse=No
 
 
 # A step of a few tokens runs for a few microseconds on the GPU, so these calls
-# are written for the host's time: one struct constructor, no formatted messages
-# before a failure, and the raw stream and device numbers.
+# are written for the host's time: the parameters packed in one call, no
+# formatted messages before a failure, the raw stream and device numbers.
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+
+
+def _packer(params):
+    """The bytes of a parameter struct from its fields in order (pointers as ints, 0 for NULL)."""
+    codes = {_vp: "P", _i32: "i", _i64: "q", ctypes.c_float: "f"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in params._fields_)).pack
+
+
+_pack_plan, _pack_rotary, _pack_append = _packer(PlanParams), _packer(RotaryParams), _packer(AppendParams)
+_pack_gather, _pack_decode, _pack_prefill = _packer(GatherParams), _packer(DecodeParams), _packer(PrefillParams)
 
 
 def _device_index(first, *others) -> int:
@@ -695,47 +705,50 @@ def _device_index(first, *others) -> int:
     return index
 
 
-def _call(fn, where, index, *args):
-    """fn(*args, stream) on the current stream of device ``index``, with that device current."""
+def _call(fn, where, index, p):
+    """fn(p, stream) on the current stream of device ``index``, with that device current."""
     if torch._C._cuda_getDevice() == index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        status = fn(p, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != ATTN_OK:
+            status = fn(p, torch._C._cuda_getCurrentRawStream(index))
+    if status:
         raise AttnError(status, where)
 
 
-def _call_with_workspace(fn, where, index, p, k_scales, v_scales, workspace):
-    """Query the workspace size, take the caller's workspace or a new one, and launch."""
+def _call_with_workspace(fn, where, index, p, ks, vs, workspace, device):
+    """The launch, with the caller's workspace or, where the call needs one, a new one."""
     if torch._C._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return _call_with_workspace(fn, where, index, p, k_scales, v_scales, workspace)
-    ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+            return _call_with_workspace(fn, where, index, p, ks, vs, workspace, device)
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if workspace is None:
-        need = ctypes.c_size_t(0)
-        _check(fn(p, ks, vs, None, 0, need, None), where)
-        if need.value:
-            workspace = torch.empty(need.value, dtype=torch.uint8, device=k_scales.device)
-    if workspace is None:
-        ptr, size = None, 0
-    else:
-        ptr, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(fn(p, ks, vs, ptr, size, None, torch._C._cuda_getCurrentRawStream(index)), where)
+        status = fn(p, ks, vs, None, 0, None, stream)  # enqueues nothing if it needs a workspace
+        if status == ATTN_ERR_WORKSPACE:
+            need = ctypes.c_size_t(0)
+            _check(fn(p, ks, vs, None, 0, need, None), where)
+            workspace = torch.empty(need.value, dtype=_U8, device=device)
+    if workspace is not None:
+        status = fn(p, ks, vs, workspace.data_ptr(), workspace.numel() * workspace.element_size(), None, stream)
+    if status:
+        raise AttnError(status, where)
 
 
 def _i32_vec(t, n, what):
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype is not _I32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"int32 {what} [{n}]")
 
 
 def _table(t, batch):
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != batch or not t.is_contiguous():
+    """Checks a block table; returns its columns."""
+    shape = t.shape
+    if t.dtype is not _I32 or len(shape) != 2 or shape[0] != batch or not t.is_contiguous():
         raise ValueError("int32 block table [B, max_blocks]")
+    return shape[1]
 
 
 def _opt(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, total_q: int, num_blocks: int,
@@ -759,21 +772,20 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     B, total_q = seq_lens.numel(), int(total_q)
     if total_q < 0:
         raise ValueError("total_q >= 0")
-    _table(block_table, B)
-    num_free = free_blocks.numel()
+    columns, num_free = _table(block_table, B), free_blocks.numel()
     _i32_vec(free_blocks, num_free, "free_blocks")
+    _i32_vec(seq_lens, B, "seq_lens")
     new = seq_lens.new_empty
     if seq_lens_out is None:
-        seq_lens_out = new(B, dtype=torch.int32)
+        seq_lens_out = new(B)
     if cu_seqlens_q is None:
-        cu_seqlens_q = new(B + 1, dtype=torch.int32)
+        cu_seqlens_q = new(B + 1)
     if positions is None:
-        positions = new(total_q, dtype=torch.int32)
+        positions = new(total_q)
     if slot_map is None:
-        slot_map = new(total_q, dtype=torch.int32)
+        slot_map = new(total_q)
     if num_used_out is None:
-        num_used_out = new(1, dtype=torch.int32)
-    _i32_vec(seq_lens, B, "seq_lens")
+        num_used_out = new(1)
     _i32_vec(new_lens, B, "new_lens")
     _i32_vec(num_used, 1, "num_used")
     _i32_vec(seq_lens_out, B, "seq_lens_out")
@@ -781,10 +793,10 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     _i32_vec(positions, total_q, "positions")
     _i32_vec(slot_map, total_q, "slot_map")
     _i32_vec(num_used_out, 1, "num_used_out")
-    p = PlanParams(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
+    p = _pack_plan(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
                    num_used.data_ptr(), seq_lens_out.data_ptr(), cu_seqlens_q.data_ptr(), positions.data_ptr(),
-                   slot_map.data_ptr(), num_used_out.data_ptr(), _opt(error_flags), B, block_table.shape[1],
-                   int(num_blocks), num_free, total_q, 16)
+                   slot_map.data_ptr(), num_used_out.data_ptr(), _opt(error_flags), B, columns, int(num_blocks),
+                   num_free, total_q, 16)
     _call(LIB.attn_plan_paged_step, "attn_plan_paged_step", index, p)
     return seq_lens_out, cu_seqlens_q, positions, slot_map, num_used_out
 
@@ -832,18 +844,18 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: b
     else:
         raise ValueError("q must be [B, Hq, S, D] or packed [T, Hq, D]")
     if q_out is None:
-        q_out = q.new_empty(shape, dtype=out_dtype)
+        q_out = q.new_empty(shape) if out_dtype is None else q.new_empty(shape, dtype=out_dtype)
     xs, ys = q.stride(), q_out.stride()
     if q_out.shape != shape or xs[-1] != 1 or ys[-1] != 1:
         raise ValueError("q_out of q's shape; last dims contiguous")
     qv, qo = ((0, xs[1], xs[0]), (0, ys[1], ys[0])) if packed else (xs[:3], ys[:3])
     in_code, out_code = _row_code(q.dtype), _row_code(q_out.dtype)
     if k is None:
-        Hk, k_ptr, ko_ptr, kv, ko = 0, None, None, (0, 0, 0), (0, 0, 0)
+        Hk, k_ptr, ko_ptr, kv, ko = 0, 0, 0, (0, 0, 0), (0, 0, 0)
     else:
         kshape = k.shape
         if k_out is None:
-            k_out = k.new_empty(kshape, dtype=out_dtype)
+            k_out = k.new_empty(kshape) if out_dtype is None else k.new_empty(kshape, dtype=out_dtype)
         xs, ys = k.stride(), k_out.stride()
         if len(kshape) != len(shape) or kshape[-1] != D or kshape[0] != shape[0] or (not packed and kshape[2] != S):
             raise ValueError("k of q's rows and head_dim")
@@ -855,7 +867,7 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: b
         Hk, k_ptr, ko_ptr = kshape[1], k.data_ptr(), k_out.data_ptr()
     if positions is not None:
         _i32_vec(positions, B * S, "positions")
-    p = RotaryParams(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, _opt(positions), inv_freq.data_ptr(), B, Hq, Hk,
+    p = _pack_rotary(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, _opt(positions), inv_freq.data_ptr(), B, Hq, Hk,
                      S, D, rotary_dim, 1 if interleaved else 0, 1 if inverse else 0, magnitude, in_code, out_code,
                      *qv, *kv, *qo, *ko)
     _call(LIB.attn_rotary, "attn_rotary", index, p)
@@ -863,21 +875,21 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: b
 
 
 def _pool(k_cache, v_cache, k_scales, v_scales):
-    """Checks a paged cache; returns (num_blocks, Hkv, D, dtype code)."""
+    """Checks a paged cache; returns (num_blocks, Hkv, D, dtype code, pointers of the scales)."""
     shape, dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or shape[2] != 16 or v_cache.shape != shape or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache [num_blocks, Hkv, 16, D] of one dtype")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("contiguous caches")
     NB, Hkv, _, D = shape
-    if dtype is torch.bfloat16:
-        return NB, Hkv, D, ATTN_DTYPE_BF16
-    if dtype is not torch.uint8 and dtype is not torch.float8_e4m3fn:
+    if dtype is _BF16:
+        return NB, Hkv, D, ATTN_DTYPE_BF16, 0, 0
+    if dtype is not _U8 and dtype is not torch.float8_e4m3fn:
         raise ValueError("bf16 or E4M3 caches")
     for t in (k_scales, v_scales):
-        if t is None or t.dtype is not torch.uint8 or t.shape != shape[:2] or not t.is_contiguous():
+        if t is None or t.dtype is not _U8 or t.shape != shape[:2] or not t.is_contiguous():
             raise ValueError("uint8 scales [num_blocks, Hkv]")
-    return NB, Hkv, D, ATTN_DTYPE_FP8_E4M3
+    return NB, Hkv, D, ATTN_DTYPE_FP8_E4M3, k_scales.data_ptr(), v_scales.data_ptr()
 
 
 def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None, q=None, inv_freq=None, positions=None,
@@ -896,18 +908,18 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
     """
     index = _device_index(k, v, slot_map, k_cache, v_cache, k_scales, v_scales, q, inv_freq, positions, q_out,
                           error_flags)
-    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, D, code, ks_ptr, vs_ptr = _pool(k_cache, v_cache, k_scales, v_scales)
     shape, ks, vs = k.shape, k.stride(), v.stride()
     if len(shape) != 3 or v.shape != shape or shape[1] != Hkv or shape[2] != D:
         raise ValueError("k, v [T, Hkv, D]")
     T = shape[0]
-    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or ks[2] != 1 or vs[2] != 1:
+    if k.dtype is not _BF16 or v.dtype is not _BF16 or ks[2] != 1 or vs[2] != 1:
         raise ValueError("bf16 k, v, last dim contiguous")
     _i32_vec(slot_map, T, "slot_map")
     if q is None:
-        q_out, q_ptr, qo_ptr, Hq, qs, qo = None, None, None, 0, (0, 0), (0, 0)
+        q_out, q_ptr, qo_ptr, Hq, qs, qo = None, 0, 0, 0, (0, 0), (0, 0)
     else:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype is not torch.bfloat16:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype is not _BF16:
             raise ValueError("bf16 q [T, Hq, D]")
         if q_out is None:
             q_out = q.new_empty(q.shape)
@@ -916,18 +928,16 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
             raise ValueError("q_out like q; last dims contiguous")
         q_ptr, qo_ptr, Hq = q.data_ptr(), q_out.data_ptr(), q.shape[1]
     if inv_freq is None:
-        rotary_dim, pos_ptr, freq_ptr = 0, None, None
+        rotary_dim, pos_ptr, freq_ptr = 0, 0, 0
     else:
         rotary_dim = _frequencies(inv_freq)
         if positions is None:
             raise ValueError("positions of the rows to turn")
         _i32_vec(positions, T, "positions")
         pos_ptr, freq_ptr = positions.data_ptr(), inv_freq.data_ptr()
-    fp8 = code == ATTN_DTYPE_FP8_E4M3
-    p = AppendParams(q_ptr, qo_ptr, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                     k_scales.data_ptr() if fp8 else None, v_scales.data_ptr() if fp8 else None, slot_map.data_ptr(),
-                     pos_ptr, freq_ptr, _opt(error_flags), T, Hq, Hkv, D, NB, 16, rotary_dim, 1 if interleaved else 0,
-                     magnitude, code, qs[0], qs[1], qo[0], qo[1], ks[0], ks[1], vs[0], vs[1])
+    p = _pack_append(q_ptr, qo_ptr, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks_ptr, vs_ptr,
+                     slot_map.data_ptr(), pos_ptr, freq_ptr, _opt(error_flags), T, Hq, Hkv, D, NB, 16, rotary_dim,
+                     1 if interleaved else 0, magnitude, code, qs[0], qs[1], qo[0], qo[1], ks[0], ks[1], vs[0], vs[1])
     _call(LIB.attn_append_paged, "attn_append_paged", index, p)
     return q_out
 
@@ -940,25 +950,23 @@ def gather_paged(k_cache, v_cache, block_table, seq_lens, width: int, k_scales=N
     seq_lens[b] on are 0.
     """
     index = _device_index(k_cache, v_cache, block_table, seq_lens, k_scales, v_scales, k_out, v_out, error_flags)
-    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, D, code, ks_ptr, vs_ptr = _pool(k_cache, v_cache, k_scales, v_scales)
     B, width = seq_lens.numel(), int(width)
-    _table(block_table, B)
+    columns = _table(block_table, B)
     _i32_vec(seq_lens, B, "seq_lens")
     if width < 0:
         raise ValueError("width >= 0")
     shape = (B, Hkv, width, D)
     if k_out is None:
-        k_out = k_cache.new_empty(shape, dtype=torch.bfloat16)
+        k_out = k_cache.new_empty(shape, dtype=_BF16)
     if v_out is None:
-        v_out = k_cache.new_empty(shape, dtype=torch.bfloat16)
+        v_out = k_cache.new_empty(shape, dtype=_BF16)
     for t in (k_out, v_out):
-        if t.shape != shape or t.dtype is not torch.bfloat16 or not t.is_contiguous():
+        if t.shape != shape or t.dtype is not _BF16 or not t.is_contiguous():
             raise ValueError("contiguous bf16 outputs [B, Hkv, width, D]")
-    fp8 = code == ATTN_DTYPE_FP8_E4M3
-    p = GatherParams(k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr() if fp8 else None,
-                     v_scales.data_ptr() if fp8 else None, block_table.data_ptr(), seq_lens.data_ptr(),
-                     k_out.data_ptr(), v_out.data_ptr(), _opt(error_flags), B, Hkv, D, width, NB, 16,
-                     block_table.shape[1], code)
+    p = _pack_gather(k_cache.data_ptr(), v_cache.data_ptr(), ks_ptr, vs_ptr, block_table.data_ptr(),
+                     seq_lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _opt(error_flags), B, Hkv, D, width, NB,
+                     16, columns, code)
     _call(LIB.attn_gather_paged, "attn_gather_paged", index, p)
     return k_out, v_out
 
@@ -975,29 +983,29 @@ def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tab
     """
     index = _device_index(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, out, lse, workspace,
                           error_flags)
-    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, D, code, ks_ptr, vs_ptr = _pool(k_cache, v_cache, k_scales, v_scales)
     if code != ATTN_DTYPE_FP8_E4M3:
         raise ValueError("E4M3 caches")
     shape = q.shape
-    if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or not q.is_contiguous():
+    if len(shape) != 3 or shape[2] != D or q.dtype is not _BF16 or not q.is_contiguous():
         raise ValueError("contiguous bf16 q [B, Hq, D]")
     B, Hq, _ = shape
-    _table(block_table, B)
+    columns = _table(block_table, B)
     _i32_vec(seq_lens, B, "seq_lens")
     if out is None:
         out = q.new_empty(shape, dtype=out_dtype)
     elif out.shape != shape or not out.is_contiguous():
         raise ValueError("contiguous out [B, Hq, D]")
     if lse is None:
-        lse = q.new_empty((B, Hq), dtype=torch.float32) if want_lse else None
-    elif lse.shape != shape[:2] or lse.dtype is not torch.float32 or not lse.is_contiguous():
+        lse = q.new_empty((B, Hq), dtype=_F32) if want_lse else None
+    elif lse.shape != shape[:2] or lse.dtype is not _F32 or not lse.is_contiguous():
         raise ValueError("contiguous fp32 lse [B, Hq]")
-    p = DecodeParams(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                     out.data_ptr(), _opt(lse), B, Hq, Hkv, D, 16, block_table.shape[1], NB, int(max_seq_len),
-                     int(num_splits), 1.0 / math.sqrt(D) if scale is None else scale, _row_code(out.dtype),
-                     _opt(error_flags), code, 1.0, 1.0)
-    _call_with_workspace(LIB.attn_decode_paged_block_scaled, "attn_decode_paged_block_scaled", index, p, k_scales,
-                         v_scales, workspace)
+    p = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                     out.data_ptr(), _opt(lse), B, Hq, Hkv, D, 16, columns, NB, int(max_seq_len), int(num_splits),
+                     1.0 / math.sqrt(D) if scale is None else scale, _row_code(out.dtype), _opt(error_flags), code, 1.0,
+                     1.0)
+    _call_with_workspace(LIB.attn_decode_paged_block_scaled, "attn_decode_paged_block_scaled", index, p, ks_ptr,
+                         vs_ptr, workspace, k_scales.device)
     return out, lse
 
 
@@ -1012,27 +1020,46 @@ def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_ta
     """
     index = _device_index(q, k_cache, v_cache, k_scales, v_scales, block_table, seqlens_k, seqlens_q, out, lse,
                           workspace, error_flags, cu_seqlens_q)
-    NB, Hkv, D, code = _pool(k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, D, code, ks_ptr, vs_ptr = _pool(k_cache, v_cache, k_scales, v_scales)
     if code != ATTN_DTYPE_FP8_E4M3:
         raise ValueError("E4M3 caches")
-    if q.shape[-1] != D:
-        raise ValueError("caches of q's head_dim")
-    B = seqlens_k.numel()
-    _table(block_table, B)
+    shape, B = q.shape, seqlens_k.numel()
+    columns = _table(block_table, B)
     _i32_vec(seqlens_k, B, "seqlens_k")
-    if seqlens_q is not None:
-        _i32_vec(seqlens_q, B, "seqlens_q")
-    p = PrefillParams()
-    out, lse = _queries(p, q, out, lse, out_dtype, want_lse, B, cu_seqlens_q, max_seqlen_q)
-    p.k_cache, p.v_cache, p.block_table = k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
-    p.seqlens_k, p.seqlens_q = seqlens_k.data_ptr(), _opt(seqlens_q)
-    p.batch, p.num_kv_heads = B, Hkv
-    p.seqlen_k = block_table.shape[1] * 16 if max_seqlen_k is None else int(max_seqlen_k)
-    p.max_blocks_per_seq, p.num_blocks, p.block_size = block_table.shape[1], NB, 16
-    p.scale, p.causal = 1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0
-    p.error_flags = _opt(error_flags)
-    _call_with_workspace(LIB.attn_prefill_paged_block_scaled, "attn_prefill_paged_block_scaled", index, p, k_scales,
-                         v_scales, workspace)
+    packed = cu_seqlens_q is not None
+    if packed:
+        if len(shape) != 3 or seqlens_q is not None or max_seqlen_q is None:
+            raise ValueError("packed q [total_q, Hq, D] with max_seqlen_q and without seqlens_q")
+        _i32_vec(cu_seqlens_q, B + 1, "cu_seqlens_q")
+        total, Hq, _ = shape
+        Sq, lse_shape = int(max_seqlen_q), (Hq, total)
+    else:
+        if len(shape) != 4 or shape[0] != B:
+            raise ValueError("q [B, Hq, Sq, D]")
+        if seqlens_q is not None:
+            _i32_vec(seqlens_q, B, "seqlens_q")
+        _, Hq, Sq, _ = shape
+        total, lse_shape = 0, shape[:3]
+    qs = q.stride()
+    if shape[-1] != D or q.dtype is not _BF16 or qs[-1] != 1:
+        raise ValueError("bf16 q of the caches' head_dim, last dim contiguous")
+    if out is None:
+        out = q.new_empty(shape, dtype=out_dtype)
+    os = out.stride()
+    if out.shape != shape or os[-1] != 1:
+        raise ValueError("out of q's shape, last dim contiguous")
+    if lse is None:
+        lse = q.new_empty(lse_shape, dtype=_F32) if want_lse else None
+    elif lse.shape != lse_shape or lse.dtype is not _F32 or not lse.is_contiguous():
+        raise ValueError("contiguous fp32 lse [B, Hq, Sq] or packed [Hq, total_q]")
+    qv, ov = ((0, qs[1], qs[0]), (0, os[1], os[0])) if packed else (qs[:3], os[:3])
+    p = _pack_prefill(q.data_ptr(), 0, 0, out.data_ptr(), _opt(lse), B, Hq, Hkv, D, Sq,
+                      columns * 16 if max_seqlen_k is None else int(max_seqlen_k), *qv, 0, 0, 0, 0, 0, 0, *ov,
+                      1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, _row_code(out.dtype),
+                      _opt(seqlens_q), seqlens_k.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                      block_table.data_ptr(), columns, NB, 16, _opt(error_flags), _opt(cu_seqlens_q), total)
+    _call_with_workspace(LIB.attn_prefill_paged_block_scaled, "attn_prefill_paged_block_scaled", index, p, ks_ptr,
+                         vs_ptr, workspace, k_scales.device)
     return out, lse
 
 

@@ -78,12 +78,12 @@ struct Lanes {
 };
 
 // Starts the copies of the lane's rows of a run (as in write_run) to its slots of a stage.
-template <int D, bool INTER>
+template <int D>
 __device__ __forceinline__ void fetch_run(const __nv_bfloat16* x, long long rs, int rotary_dim, int t, int n, int off0,
                                           uint4 (*stage)[THREADS]) {
   using L = Lanes<D>;
   const L l;
-  const int2 off = rotary::unit_offsets<INTER>(l.u, rotary_dim);
+  const int2 off = rotary::unit_offsets<D>(l.u, rotary_dim);
 #pragma unroll
   for (int i = 0; i < L::PER; ++i) {
     const int o = l.grp + L::GROUPS * i;
@@ -110,7 +110,7 @@ __device__ __forceinline__ void write_run(const uint4 (*stage)[THREADS],
   const L l;
   const int lane = lane_id(), pair = warp_id() / 2, half = warp_id() & 1, u = l.u, grp = l.grp;
   const bool turned = turn && u * 16 < rotary_dim;
-  const int2 off = rotary::unit_offsets<INTER>(u, turn ? rotary_dim : 0);
+  const int2 off = rotary::unit_offsets<D>(u, turn ? rotary_dim : 0);
   const int old_byte = FP8 && off0 > 0 ? *scale : -1;
   const float old_scale = old_byte >= 0 ? bscale::scale_of(old_byte) : 0.f;
   float val[PER][16];
@@ -136,7 +136,7 @@ __device__ __forceinline__ void write_run(const uint4 (*stage)[THREADS],
     const int o = grp + GROUPS * i;
     if (turned && o >= off0 && o < off0 + n) {
       float c[8], s[8];
-      rotary::unit_turn(turn[o - off0], u, c, s);
+      rotary::unit_turn<INTER>(turn[o - off0], u, rotary_dim, c, s);
       rotary::UnitTurn ut;
       ut.set(c, s);
       rotary::turn16<INTER>(val[i], ut);
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
       run_of(c, i, n);
       const int off0 = __shfl_sync(FULL, slot, i) % BS, h = h0 + (c.it >> 1);
       const bool is_v = c.it & 1;
-      fetch_run<D, INTER>(is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs, is_v ? a.v_rs : a.k_rs, is_v ? 0 : rotary_dim,
+      fetch_run<D>(is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs, is_v ? a.v_rs : a.k_rs, is_v ? 0 : rotary_dim,
                           (int)(first - 1 + i), n, off0, sm.ring[stage]);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -413,13 +413,15 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
     a.q_blocks = (int)q_blocks;
   }
   // A CTA per row while that does not fill the machine (a decode step has one
-  // run per row), per 16 rows beyond (a chunk has one run per 16); a window's
-  // heads go to as many CTAs as run at once, a head each for a pair of warps at
-  // the least.
+  // run per row), per 16 rows beyond (a chunk has one run per 16). A window's
+  // heads are shared out to four times as many CTAs as run at once, down to two
+  // heads each (one run for each pair of warps): a window with a second run, at
+  // a sequence's start, then ends with the others, for angles that several CTAs
+  // compute (8504 rows of 8 heads: all heads 25 us, 4 heads 21 us, 2 heads 20 us).
   a.window = p.total <= 2 * sms ? 1 : 16;
   const long long windows = (p.total + a.window - 1) / a.window;
   const int most = (p.num_kv_heads + 1) / 2;  // two heads: a head of K or V for each pair
-  const long long chunks = 4LL * sms / windows;
+  const long long chunks = 16LL * sms / windows;
   a.heads_per = (int)(chunks >= most ? 2 : chunks > 1 ? (p.num_kv_heads + chunks - 1) / chunks : p.num_kv_heads);
   a.head_chunks = (p.num_kv_heads + a.heads_per - 1) / a.heads_per;
   const long long blocks = a.q_blocks + windows * a.head_chunks;

@@ -1,11 +1,12 @@
 // Rotary positions: the turn of 16 row elements by one thread, shared by the
 // rotary kernel and the cache append.
 //
-// A row of head_dim elements is cut into head_dim / 16 units. A unit below
-// rotary_dim / 16 turns the pairs 8 u .. 8 u + 7, whichever way the pairs lie
-// (half layout: elements 8 u .. and rotary_dim / 2 + 8 u ..; interleaved: 16 u
-// .. 16 u + 15); the units above copy 16 elements. Either way a thread moves two
-// 8-element vectors per row and reuses its 8 angles for every head of a token.
+// A row of head_dim elements is cut into head_dim / 16 units of two 8-element
+// vectors. A unit below rotary_dim / 16 owns elements 8 u .. 8 u + 7 and
+// rotary_dim / 2 + 8 u .. + 7 of the turned part: 8 pairs, whichever way they lie
+// (half layout: pairs 8 u .., an element from each vector; interleaved: 4 pairs
+// in each vector). The other units own the rest in the same way, so that
+// neighbouring lanes always move neighbouring 16 bytes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -24,10 +25,19 @@ struct Turn {
 };
 
 // Element offsets of a unit's two 8-element vectors.
-template <bool INTER>
+template <int D>
 __device__ __forceinline__ int2 unit_offsets(int u, int rotary_dim) {
-  if (!INTER && u * 16 < rotary_dim) return make_int2(8 * u, rotary_dim / 2 + 8 * u);
-  return make_int2(16 * u, 16 * u + 8);
+  const bool in_turned = u * 16 < rotary_dim;
+  const int v = in_turned ? u : u - rotary_dim / 16;
+  const int first = in_turned ? 0 : rotary_dim, half = (in_turned ? rotary_dim : D - rotary_dim) / 2;
+  return make_int2(first + 8 * v, first + half + 8 * v);
+}
+
+// The i-th of a turned unit's 8 pairs.
+template <bool INTER>
+__device__ __forceinline__ int unit_pair(int u, int i, int rotary_dim) {
+  if (!INTER) return 8 * u + i;
+  return 4 * u + i + (i < 4 ? 0 : rotary_dim / 4 - 4);
 }
 
 // magnitude * (cos, sin) of position * inv_freq[pair]. The angle is reduced to
@@ -45,11 +55,11 @@ __device__ __forceinline__ float2 pair_turn(const Turn& t, int position, int pai
 constexpr int MAX_PAIRS = 64;
 
 // The angles of unit u out of a row of them.
-__device__ __forceinline__ void unit_turn(const float2* row, int u, float (&c)[8], float (&s)[8]) {
-  const float4* cs = reinterpret_cast<const float4*>(row + 8 * u);
+template <bool INTER>
+__device__ __forceinline__ void unit_turn(const float2* row, int u, int rotary_dim, float (&c)[8], float (&s)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 y = cs[j];
+    const float4 y = *reinterpret_cast<const float4*>(row + unit_pair<INTER>(u, 2 * j, rotary_dim));
     c[2 * j] = y.x, s[2 * j] = y.y, c[2 * j + 1] = y.z, s[2 * j + 1] = y.w;
   }
 }
@@ -184,9 +194,10 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile
   const int group = group_index * W::HEADS + hsub, step = r.head_groups * W::HEADS;
   const int b = token / r.seqlen, pos_in_seq = token - b * r.seqlen;
   const bool turned = u * 16 < t.rotary_dim;
-  const int2 off = unit_offsets<INTER>(u, t.rotary_dim);
-  const TI* q = reinterpret_cast<const TI*>(r.q) + b * r.q_bs + pos_in_seq * r.q_rs;
-  const TI* k = reinterpret_cast<const TI*>(r.k) + b * r.k_bs + pos_in_seq * r.k_rs;
+  const int2 off = unit_offsets<D>(u, t.rotary_dim);
+  const int second = off.y - off.x;  // from the unit's first vector to its second
+  const TI* q = reinterpret_cast<const TI*>(r.q) + b * r.q_bs + pos_in_seq * r.q_rs + off.x;
+  const TI* k = reinterpret_cast<const TI*>(r.k) + b * r.k_bs + pos_in_seq * r.k_rs + off.x;
   Ring<TI> ring(smem);
   // The next row to fetch: its head, counted on through q and k, and its address.
   int fetch_h = live ? group : r.heads;
@@ -194,7 +205,7 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile
   long long fetch_step = step * (group < r.hq ? r.q_hs : r.k_hs);
   auto fetch = [&](int stage) {
     if (fetch_h < r.heads) {
-      ring.fetch(stage, fetch_at + off.x, fetch_at + off.y);
+      ring.fetch(stage, fetch_at, fetch_at + second);
       const bool was_q = fetch_h < r.hq;
       fetch_h += step;
       fetch_at += fetch_step;
@@ -217,7 +228,7 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile
     float2 mine[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      mine[i] = turned && !skipped ? pair_turn(t, position, 8 * u + hsub * PER + i) : make_float2(1.f, 0.f);
+      mine[i] = turned && !skipped ? pair_turn(t, position, unit_pair<INTER>(u, hsub * PER + i, t.rotary_dim)) : make_float2(1.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       c[i] = __shfl_sync(0xffffffffu, mine[i % PER].x, i / PER * W::UNITS + u);
@@ -226,14 +237,14 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile
   } else if (turned && !skipped) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 y = pair_turn(t, position, 8 * u + i);
+      const float2 y = pair_turn(t, position, unit_pair<INTER>(u, i, t.rotary_dim));
       c[i] = y.x, s[i] = y.y;
     }
   }
   UnitTurn turn;
   turn.set(c, s);
-  TO* ko = reinterpret_cast<TO*>(r.k_out) + b * r.ko_bs + pos_in_seq * r.ko_rs;
-  TO* to = group < r.hq ? reinterpret_cast<TO*>(r.q_out) + b * r.qo_bs + pos_in_seq * r.qo_rs + group * r.qo_hs
+  TO* ko = reinterpret_cast<TO*>(r.k_out) + b * r.ko_bs + pos_in_seq * r.ko_rs + off.x;
+  TO* to = group < r.hq ? reinterpret_cast<TO*>(r.q_out) + b * r.qo_bs + pos_in_seq * r.qo_rs + group * r.qo_hs + off.x
                         : ko + (group - r.hq) * r.ko_hs;
   long long to_step = step * (group < r.hq ? r.qo_hs : r.ko_hs);
   int h = skipped ? r.heads : group;
@@ -246,8 +257,8 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile
       float x[16];
       ring.get(stage, x);
       if (turned) turn16<INTER>(x, turn);
-      store8(to + off.x, x);
-      store8(to + off.y, x + 8);
+      store8(to, x);
+      store8(to + second, x + 8);
       const bool was_q = h < r.hq;
       h += step;
       to += to_step;
