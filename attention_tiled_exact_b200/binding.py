@@ -747,6 +747,11 @@ def _table(t, batch):
     return shape[1]
 
 
+def _like(t, dtype):
+    """A new tensor of t's shape (empty_like is the cheapest way where the dtype stays)."""
+    return torch.empty_like(t) if dtype is None or dtype is t.dtype else torch.empty_like(t, dtype=dtype)
+
+
 def _opt(t):
     return 0 if t is None else t.data_ptr()
 
@@ -775,17 +780,16 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     columns, num_free = _table(block_table, B), free_blocks.numel()
     _i32_vec(free_blocks, num_free, "free_blocks")
     _i32_vec(seq_lens, B, "seq_lens")
-    new = seq_lens.new_empty
     if seq_lens_out is None:
-        seq_lens_out = new(B)
+        seq_lens_out = torch.empty(B, dtype=_I32, device=seq_lens.device)
     if cu_seqlens_q is None:
-        cu_seqlens_q = new(B + 1)
+        cu_seqlens_q = torch.empty(B + 1, dtype=_I32, device=seq_lens.device)
     if positions is None:
-        positions = new(total_q)
+        positions = torch.empty(total_q, dtype=_I32, device=seq_lens.device)
     if slot_map is None:
-        slot_map = new(total_q)
+        slot_map = torch.empty(total_q, dtype=_I32, device=seq_lens.device)
     if num_used_out is None:
-        num_used_out = new(1)
+        num_used_out = torch.empty(1, dtype=_I32, device=seq_lens.device)
     _i32_vec(new_lens, B, "new_lens")
     _i32_vec(num_used, 1, "num_used")
     _i32_vec(seq_lens_out, B, "seq_lens_out")
@@ -844,7 +848,7 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: b
     else:
         raise ValueError("q must be [B, Hq, S, D] or packed [T, Hq, D]")
     if q_out is None:
-        q_out = q.new_empty(shape) if out_dtype is None else q.new_empty(shape, dtype=out_dtype)
+        q_out = _like(q, out_dtype)
     xs, ys = q.stride(), q_out.stride()
     if q_out.shape != shape or xs[-1] != 1 or ys[-1] != 1:
         raise ValueError("q_out of q's shape; last dims contiguous")
@@ -855,7 +859,7 @@ def rotary(q, k, inv_freq, positions=None, interleaved: bool = False, inverse: b
     else:
         kshape = k.shape
         if k_out is None:
-            k_out = k.new_empty(kshape) if out_dtype is None else k.new_empty(kshape, dtype=out_dtype)
+            k_out = _like(k, out_dtype)
         xs, ys = k.stride(), k_out.stride()
         if len(kshape) != len(shape) or kshape[-1] != D or kshape[0] != shape[0] or (not packed and kshape[2] != S):
             raise ValueError("k of q's rows and head_dim")
@@ -922,7 +926,7 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
         if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype is not _BF16:
             raise ValueError("bf16 q [T, Hq, D]")
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = torch.empty_like(q)
         qs, qo = q.stride(), q_out.stride()
         if q_out.shape != q.shape or q_out.dtype is not q.dtype or qs[2] != 1 or qo[2] != 1:
             raise ValueError("q_out like q; last dims contiguous")
@@ -958,9 +962,9 @@ def gather_paged(k_cache, v_cache, block_table, seq_lens, width: int, k_scales=N
         raise ValueError("width >= 0")
     shape = (B, Hkv, width, D)
     if k_out is None:
-        k_out = k_cache.new_empty(shape, dtype=_BF16)
+        k_out = torch.empty(shape, dtype=_BF16, device=k_cache.device)
     if v_out is None:
-        v_out = k_cache.new_empty(shape, dtype=_BF16)
+        v_out = torch.empty_like(k_out)
     for t in (k_out, v_out):
         if t.shape != shape or t.dtype is not _BF16 or not t.is_contiguous():
             raise ValueError("contiguous bf16 outputs [B, Hkv, width, D]")
@@ -993,11 +997,11 @@ def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tab
     columns = _table(block_table, B)
     _i32_vec(seq_lens, B, "seq_lens")
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
+        out = _like(q, out_dtype)
     elif out.shape != shape or not out.is_contiguous():
         raise ValueError("contiguous out [B, Hq, D]")
     if lse is None:
-        lse = q.new_empty((B, Hq), dtype=_F32) if want_lse else None
+        lse = torch.empty((B, Hq), dtype=_F32, device=q.device) if want_lse else None
     elif lse.shape != shape[:2] or lse.dtype is not _F32 or not lse.is_contiguous():
         raise ValueError("contiguous fp32 lse [B, Hq]")
     p = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
@@ -1044,12 +1048,12 @@ def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_ta
     if shape[-1] != D or q.dtype is not _BF16 or qs[-1] != 1:
         raise ValueError("bf16 q of the caches' head_dim, last dim contiguous")
     if out is None:
-        out = q.new_empty(shape, dtype=out_dtype)
+        out = _like(q, out_dtype)
     os = out.stride()
     if out.shape != shape or os[-1] != 1:
         raise ValueError("out of q's shape, last dim contiguous")
     if lse is None:
-        lse = q.new_empty(lse_shape, dtype=_F32) if want_lse else None
+        lse = torch.empty(lse_shape, dtype=_F32, device=q.device) if want_lse else None
     elif lse.shape != lse_shape or lse.dtype is not _F32 or not lse.is_contiguous():
         raise ValueError("contiguous fp32 lse [B, Hq, Sq] or packed [Hq, total_q]")
     qv, ov = ((0, qs[1], qs[0]), (0, os[1], os[0])) if packed else (qs[:3], os[:3])
