@@ -890,8 +890,9 @@ def _pool(k_cache, v_cache, k_scales, v_scales):
         return NB, Hkv, D, ATTN_DTYPE_BF16, 0, 0
     if dtype is not _U8 and dtype is not torch.float8_e4m3fn:
         raise ValueError("bf16 or E4M3 caches")
+    rows = shape[:2]
     for t in (k_scales, v_scales):
-        if t is None or t.dtype is not _U8 or t.shape != shape[:2] or not t.is_contiguous():
+        if t is None or t.dtype is not _U8 or t.shape != rows or not t.is_contiguous():
             raise ValueError("uint8 scales [num_blocks, Hkv]")
     return NB, Hkv, D, ATTN_DTYPE_FP8_E4M3, k_scales.data_ptr(), v_scales.data_ptr()
 
@@ -1004,6 +1005,8 @@ def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tab
         lse = torch.empty((B, Hq), dtype=_F32, device=q.device) if want_lse else None
     elif lse.shape != shape[:2] or lse.dtype is not _F32 or not lse.is_contiguous():
         raise ValueError("contiguous fp32 lse [B, Hq]")
+    if B == 0:
+        return out, lse
     p = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                      out.data_ptr(), _opt(lse), B, Hq, Hkv, D, 16, columns, NB, int(max_seq_len), int(num_splits),
                      1.0 / math.sqrt(D) if scale is None else scale, _row_code(out.dtype), _opt(error_flags), code, 1.0,
@@ -1056,6 +1059,8 @@ def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_ta
         lse = torch.empty(lse_shape, dtype=_F32, device=q.device) if want_lse else None
     elif lse.shape != lse_shape or lse.dtype is not _F32 or not lse.is_contiguous():
         raise ValueError("contiguous fp32 lse [B, Hq, Sq] or packed [Hq, total_q]")
+    if B == 0 or out.numel() == 0:
+        return out, lse
     qv, ov = ((0, qs[1], qs[0]), (0, os[1], os[0])) if packed else (qs[:3], os[:3])
     p = _pack_prefill(q.data_ptr(), 0, 0, out.data_ptr(), _opt(lse), B, Hq, Hkv, D, Sq,
                       columns * 16 if max_seqlen_k is None else int(max_seqlen_k), *qv, 0, 0, 0, 0, 0, 0, *ov,

@@ -42,14 +42,19 @@ __device__ __forceinline__ int unit_pair(int u, int i, int rotary_dim) {
 
 // magnitude * (cos, sin) of position * inv_freq[pair]. The angle is reduced to
 // half turns in fp64 (an fp32 product is off by half a step of the angle, 0.03
-// rad at position 10^6) and only the remainder, in [-1, 1], goes to fp32.
+// rad at position 10^6); the remainder, in [-1, 1], goes to fp32 as a sum hi + lo
+// whose second part enters to first order, cos(a + d) = cos a - d sin a: rounded
+// to hi alone it would be off by up to 2^-23.3 rad, more than all that follows,
+// and an 8-bit key is made from the result.
 __device__ __forceinline__ float2 pair_turn(const Turn& t, int position, int pair) {
   constexpr double INV_PI = 0.31830988618379067154;
+  constexpr float PI = 3.14159265358979f;
   double h = (double)position * (__ldg(t.inv_freq + pair) * INV_PI);
   h -= 2.0 * rint(0.5 * h);
+  const float hi = (float)h, d = PI * (float)(h - (double)hi);
   float si, co;
-  sincospif((float)h, &si, &co);
-  return make_float2(co * t.magnitude, si * t.magnitude * t.sign);
+  sincospif(hi, &si, &co);
+  return make_float2(fmaf(-d, si, co) * t.magnitude, fmaf(d, co, si) * t.magnitude * t.sign);
 }
 
 constexpr int MAX_PAIRS = 64;

@@ -728,7 +728,9 @@ ATTN_API attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* 
  * the paged mode of attn_prefill (padded or packed queries), k_cache / v_cache
  * holding E4M3 codes. p->seqlen_k bounds seqlens_k: a longer sequence is cut
  * there and flagged (ATTN_FAULT_BAD_LENGTH). Workspace protocol as
- * attn_decode_paged.
+ * attn_decode_paged; the size depends on the device's SM count. A NaN key makes
+ * the rows that see it NaN; a NaN value may do so to other rows of its chunk
+ * (their weight of 0 meets it in a tile's product).
  */
 ATTN_API attn_status_t attn_prefill_paged_block_scaled(const attn_prefill_params* p, const uint8_t* k_scales,
                                                        const uint8_t* v_scales, void* workspace,

@@ -6,6 +6,7 @@ import ctypes
 import math
 import os
 import subprocess
+import sys
 import tempfile
 
 import pytest
@@ -588,6 +589,142 @@ def test_prefill_block_scaled_shared_items(lib, Hq, Hk):
         got, gl = runs[0][0][cu[b]:cu[b + 1]].transpose(0, 1), runs[0][1][:, cu[b]:cu[b + 1]]
         _within(got, want.reshape(Hq, rows, D), tol.reshape(Hq, rows, D) + 2.0 ** -20 * want.reshape(Hq, rows, D).abs(), f"O {b}")
         _within(gl, wl.reshape(Hq, rows), ltol.reshape(Hq, rows) + 2.0 ** -12, f"LSE {b}")
+
+
+# ---------------------------------------------------------------------------- what no case above does
+
+
+@gpu
+def test_offsets_past_32_bits(lib):
+    """Pages in the last blocks of pools of more than 4 GiB (and scales, slots to match) give the same bits as near ones."""
+    if torch.cuda.mem_get_info()[0] < 14 << 30:
+        pytest.skip("needs 14 GiB of free device memory")
+    Hk, Hq, D, nb = 8, 16, 128, (1 << 32) // (8 * 16 * 128) + 40
+    g, new = _gen(41), 40
+    qkv = torch.randn(new, Hq + 2 * Hk, D, generator=g).to(torch.bfloat16).cuda()
+    freq, pos = ref.frequencies(64).cuda(), torch.arange(new, dtype=torch.int32, device="cuda")
+    outs = []
+    pools = [torch.empty(nb, Hk, 16, D, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.full((nb, Hk), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for ids in ([2, 0, 1], [nb - 1, nb - 7, nb - 3]):
+        table = torch.tensor([ids], dtype=torch.int32, device="cuda")
+        slots = table[0, (pos // 16).long()] * 16 + pos % 16
+        args = (pools[0], pools[1], scales[0], scales[1])
+        q = lib.append_paged(qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:], slots, *args, q=qkv[:, :Hq], inv_freq=freq, positions=pos)
+        lens = _i32([new]).cuda()
+        k, v = lib.gather_paged(pools[0], pools[1], table, lens, new, *scales)
+        o, lse = lib.decode_paged_block_scaled(q[-1:].contiguous(), *args, table, lens)
+        p, _ = lib.prefill_paged_block_scaled(q, *args, table, lens, cu_seqlens_q=_i32([0, new]).cuda(), max_seqlen_q=new)
+        big = qkv.new_zeros(1, 4 * Hq, 512, D)  # many rows: the tensor-core path
+        t, _ = lib.prefill_paged_block_scaled(big, *args, table, lens, causal=False)
+        outs.append((q, k, v, o, lse, p, t))
+    for a, b in zip(*outs):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@gpu
+def test_empty_calls(lib):
+    e = lambda *s, dtype=torch.int32: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+    out = lib.plan_paged_step(e(0), e(0), e(0, 4), e(0), _i32([0]).cuda(), 0, 9)
+    assert out[1].tolist() == [0] and out[4].tolist() == [0]
+    out = lib.plan_paged_step(e(0), e(0), e(0, 4), e(0), _i32([0]).cuda(), 3, 9)
+    assert out[2].tolist() == [-1, -1, -1] and out[3].tolist() == [-1, -1, -1]
+    bf = lambda *s: e(*s, dtype=torch.bfloat16)  # noqa: E731
+    freq = ref.frequencies(64).cuda()
+    assert lib.rotary(bf(0, 4, 64), bf(0, 2, 64), freq)[0].shape == (0, 4, 64)
+    assert lib.rotary(bf(2, 4, 0, 64), None, freq)[0].shape == (2, 4, 0, 64)
+    pool, sc = e(5, 2, 16, 64, dtype=torch.uint8), e(5, 2, dtype=torch.uint8)
+    assert lib.append_paged(bf(0, 2, 64), bf(0, 2, 64), e(0), pool, pool, sc, sc, q=bf(0, 4, 64)).shape == (0, 4, 64)
+    assert lib.gather_paged(pool, pool, e(0, 3), e(0), 16, sc, sc)[0].shape == (0, 2, 16, 64)
+    o, lse = lib.decode_paged_block_scaled(bf(0, 4, 64), pool, pool, sc, sc, e(0, 3), e(0))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    o, lse = lib.prefill_paged_block_scaled(bf(0, 4, 64), pool, pool, sc, sc, e(1, 3), _i32([0]).cuda(),
+                                            cu_seqlens_q=_i32([0, 0]).cuda(), max_seqlen_q=0)
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+
+
+@gpu
+@pytest.mark.parametrize("chunk", [2, 200])
+def test_rows_behind_the_last_sequence_are_left_alone(lib, chunk):
+    c = _decode_case([700, 300], 8, 2, 128, 42)
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
+    q = torch.randn(2 * chunk + 5, 8, 128, generator=_gen(1)).to(torch.bfloat16).cuda()
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, q.shape[0]), 7.0, dtype=torch.float32, device="cuda")
+    lib.prefill_paged_block_scaled(q, *dev, _i32(c["lens"]).cuda(), out=out, lse=lse,
+                                   cu_seqlens_q=_i32([0, chunk, 2 * chunk]).cuda(), max_seqlen_q=chunk)
+    assert (out[2 * chunk:] == 7.0).all() and (lse[:, 2 * chunk:] == 7.0).all()
+    assert (out[: 2 * chunk] != 7.0).any(-1).all() and torch.isfinite(lse).all()
+
+
+@gpu
+@pytest.mark.parametrize("chunk,context", [(3, 900), (200, 2000)])
+def test_prefill_block_scaled_in_a_graph_and_on_two_streams(lib, chunk, context):
+    """Captured and replayed, and two calls at once on two streams: the bits of a call by itself."""
+    cases = []
+    for seed in (51, 52):
+        c = _decode_case([chunk + context, chunk + context // 3], 8, 2, 128, seed)
+        q = torch.randn(2, 8, chunk, 128, generator=_gen(seed)).to(torch.bfloat16).cuda()
+        dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
+        cases.append(lambda q=q, dev=dev, lens=_i32(c["lens"]).cuda(): lib.prefill_paged_block_scaled(q, *dev, lens))
+    want = [f() for f in cases]
+    torch.cuda.synchronize()
+    graphs = []
+    for f in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = f()
+        graphs.append((g, out))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        both = []
+        for f, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                both.append(f())
+        torch.cuda.synchronize()
+        for w, (_, o), e in zip(want, graphs, both):
+            assert torch.equal(w[0], o[0]) and torch.equal(w[1], o[1]) and torch.equal(w[0], e[0]) and torch.equal(w[1], e[1])
+
+
+@gpu
+def test_decode_block_scaled_strided_views_are_refused(lib):
+    c = _decode_case([40, 40], 4, 2, 64, 60)
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
+    lens, q = _i32(c["lens"]).cuda(), c["q"].cuda()
+    wide = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    for args in ((wide[:, :, :64], *dev, lens), (q, dev[0].transpose(0, 1), *dev[1:], lens),
+                 (q, dev[0], dev[1], dev[2].int(), *dev[3:], lens), (q, *dev, lens.long()), (q.float(), *dev, lens),
+                 (q, *dev[:4], dev[4][:1], lens)):
+        with pytest.raises(ValueError):
+            lib.decode_paged_block_scaled(*args)
+
+
+@gpu
+def test_debug_build_finds_nothing(lib):
+    """The bounds-checking build over decode (one and several clusters) and both prefill paths: no flag."""
+    code = """
+import sys; sys.path.insert(0, %r)
+import torch
+from attention_tiled_exact_b200 import binding as lib
+from tests import test_paged_cache as t
+assert lib.debug_bounds_enabled()
+for splits in (0, 1, 16):
+    assert t._decode_run(lib, t._decode_case([1, 0, 2500, 300], 9, 3, 128, 1), num_splits=splits)[2] == 0
+c = t._decode_case([900, 40], 4, 2, 64, 2)
+dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
+for rows in (3, 400):
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 4, rows, 64, dtype=torch.bfloat16, device="cuda")
+    lib.prefill_paged_block_scaled(q, *dev, t._i32(c["lens"]).cuda(), error_flags=flags)
+    assert int(flags.item()) == 0
+print("clean")
+""" % ROOT
+    env = dict(os.environ, ATTN_B200_DEBUG_BOUNDS="1")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=600, env=env, cwd=ROOT)
+    assert r.returncode == 0 and "clean" in r.stdout, r.stdout + r.stderr
 
 
 # ---------------------------------------------------------------------------- together
