@@ -52,7 +52,7 @@ struct Append {
   const int32_t* positions;
   int32_t* flags;
   int total, hkv, num_slots;
-  int window;      // rows whose runs one CTA handles: 1 or 16
+  int window;      // rows whose runs one CTA handles, at most 16
   int heads_per;   // kv heads of a CTA
   int head_chunks; // CTAs that share a window's heads
 };
@@ -412,15 +412,19 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
     if (q_blocks > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
     a.q_blocks = (int)q_blocks;
   }
-  // A CTA per row while that does not fill the machine (a decode step has one
-  // run per row), per 16 rows beyond (a chunk has one run per 16). A window's
-  // heads are shared out to four times as many CTAs as run at once, down to two
-  // heads each (one run for each pair of warps): a window with a second run, at
-  // a sequence's start, then ends with the others, for angles that several CTAs
-  // compute (8504 rows of 8 heads: all heads 25 us, 4 heads 21 us, 2 heads 20 us).
-  a.window = p.total <= 2 * sms ? 1 : 16;
-  const long long windows = (p.total + a.window - 1) / a.window;
+  // Rows per CTA: as few as keep the grid within two rounds, 16 at most. A decode
+  // step has a run per row, and a CTA's runs follow one another; a chunk has one
+  // run per 16 rows, and CTAs without one end at once. (512 rows of 8 heads, a
+  // sequence each: 2 rows 15 us, 16 rows 30 us; a chunk of about 2000 rows: 8 rows
+  // 7 us, 1 row 11 us.) A window's heads are shared out to up to 16 CTAs per SM,
+  // down to two heads each (one run for each pair of warps): a window with a
+  // second run, at a sequence's start, then ends with the others, for angles that
+  // several CTAs compute (8504 rows of 8 heads: all heads 25 us, 4 heads 21 us, 2
+  // heads 20 us).
   const int most = (p.num_kv_heads + 1) / 2;  // two heads: a head of K or V for each pair
+  a.window = 1;
+  while (a.window < cache::BS && ((long long)p.total + a.window - 1) / a.window * most > 8LL * sms) a.window *= 2;
+  const long long windows = ((long long)p.total + a.window - 1) / a.window;
   const long long chunks = 16LL * sms / windows;
   a.heads_per = (int)(chunks >= most ? 2 : chunks > 1 ? (p.num_kv_heads + chunks - 1) / chunks : p.num_kv_heads);
   a.head_chunks = (p.num_kv_heads + a.heads_per - 1) / a.heads_per;
