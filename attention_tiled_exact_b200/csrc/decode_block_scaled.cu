@@ -782,7 +782,7 @@ bool prefill_has_few_rows(const attn_prefill_params& p) {
   const double blocks = (len + BS - 1) / BS, wide = p.head_dim / 128.0;
   const double few = 4000 + p.batch * tiles * (double)p.num_kv_heads * blocks * (p.head_dim == 128 ? 1.1 : 0.45);
   const double dense = (len > 512 ? 20000 : 9000) + p.batch * (double)p.num_kv_heads * len * wide * 0.154 +
-                       p.batch * (double)((p.seqlen_q + 127) / 128) * p.num_q_heads / 2 * ((len + 127) / 128) * 15 * wide;
+                       (double)prefill_split_items(p) * ((len + 127) / 128) * 15 * wide;
   return few < dense;
 }
 

@@ -69,6 +69,7 @@ attn_status_t launch_prefill(const attn_prefill_params& p, cudaStream_t stream);
 // workspace (prefill_split_workspace_bytes of the same parameters, 16-byte aligned).
 attn_status_t launch_prefill_behind(const attn_prefill_params& p, void* split_workspace, cudaStream_t stream);
 size_t prefill_split_workspace_bytes(const attn_prefill_params& p);
+long long prefill_split_items(const attn_prefill_params& p);  // its items, each up to 256 rows over all their keys
 
 // Non-blocking streams of the current device (which = 0 or 1), created once
 // and kept for the process: the extra streams of calls that overlap kernels

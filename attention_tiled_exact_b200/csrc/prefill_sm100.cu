@@ -46,6 +46,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "exp2_poly.cuh"
 #include "bounds_check.cuh"
 #include "internal.h"
@@ -121,6 +123,7 @@ struct Args {
   float* part_o;    // [CTA][2][tile][D / 4][BM][4], normalised: a warp's rows side by side
   float* part_lse;  // [CTA][2][tile][BM], natural log
   int4* shares;     // [CTA]: see split_items
+  int row_bits;     // a tile's 128 rows are 128 >> row_bits heads of 1 << row_bits query rows
   // paged keys/values (PAGED kernels only)
   const int32_t* block_table;
   int max_blocks;
@@ -157,34 +160,33 @@ struct Work {
   int active[2];
   int n_kv[2];  // key blocks of BK each
   int sq, sk;
-  int lo;     // SPLIT: first key block of this piece (n_kv then counts the piece's blocks)
-  bool part;  // SPLIT: the piece is not the whole item
 };
+
+// SPLIT: a piece of an item; n_kv counts the piece's blocks.
+struct Piece : Work {
+  int lo;     // first key block
+  bool part;  // the piece is not the whole item
+};
+__device__ __forceinline__ int first_block(const Work&) { return 0; }
+__device__ __forceinline__ int first_block(const Piece& w) { return w.lo; }
+__device__ __forceinline__ bool is_part(const Work&) { return false; }
+__device__ __forceinline__ bool is_part(const Piece& w) { return w.part; }
 
 template <bool SPLIT = false>
 __device__ __forceinline__ Work decode_work(const Args& a, int item) {
   Work w;
-  if (SPLIT && a.pair_heads) {
-    // fd_outer: row blocks * pairs, fd_mid: pairs, fd_inner: hkv. Neighbouring
-    // items share their keys.
+  if (SPLIT) {
+    // fd_outer: blocks of query rows * sets of heads, fd_mid: sets, fd_inner: hkv.
+    // Both tiles have the set's heads, the second one the query rows behind the
+    // first one's. Neighbouring items share their keys.
     const int q0 = a.fd_outer.div(item);
     const int r = item - q0 * a.fd_outer.d;
     const int q1 = a.fd_mid.div(r);
     w.b = a.fd_inner.div(q0);
     w.kvh = q0 - w.b * a.hkv;
-    w.head[0] = w.kvh * a.group + 2 * (r - q1 * a.fd_mid.d);
-    w.head[1] = w.head[0] + 1;
-    w.row0[0] = w.row0[1] = (a.n_row_blocks - 1 - q1) * BM;
-  } else if (SPLIT) {
-    // fd_outer: row-block pairs, fd_mid: hq, fd_inner: group
-    const int q0 = a.fd_outer.div(item);
-    const int p = a.fd_outer.d - 1 - (item - q0 * a.fd_outer.d);
-    w.b = a.fd_mid.div(q0);
-    const int h = q0 - w.b * a.hq;
-    w.kvh = a.fd_inner.div(h);
-    w.head[0] = w.head[1] = h;
-    w.row0[0] = 2 * p * BM;
-    w.row0[1] = (2 * p + 1) * BM;
+    w.head[0] = w.head[1] = w.kvh * a.group + ((r - q1 * a.fd_mid.d) << (7 - a.row_bits));
+    w.row0[0] = (a.n_row_blocks - 1 - q1) << (a.row_bits + 1);
+    w.row0[1] = w.row0[0] + (1 << a.row_bits);
   } else if (a.pair_heads) {
     // fd_outer: batch * hkv * pairs, fd_mid: pairs, fd_inner: hkv
     const int pairs = a.fd_mid.d;
@@ -234,14 +236,12 @@ __device__ __forceinline__ Work decode_work(const Args& a, int item) {
     w.active[t] = w.row0[t] < w.sq;
     int kend = w.sk;
     if (a.causal) {
-      const int last_row = min(w.row0[t] + BM, w.sq) - 1;
+      const int last_row = min(w.row0[t] + (SPLIT ? 1 << a.row_bits : BM), w.sq) - 1;
       const int lim = last_row + (w.sk - w.sq) + 1;  // keys [0, lim) visible to the tile's last row
       kend = max(0, min(w.sk, lim));
     }
     w.n_kv[t] = w.active[t] ? (kend + BK - 1) / BK : 0;
   }
-  w.lo = 0;
-  w.part = false;
   return w;
 }
 
@@ -370,7 +370,7 @@ __device__ void split_items(const Args& a, int n_items, int* cost, int* share) {
 }
 
 // The piece of item w that lies in the CTA's share.
-__device__ __forceinline__ void clip_work(Work& w, int item, const int* share) {
+__device__ __forceinline__ void clip_work(Piece& w, int item, const int* share) {
   const int n = max(w.n_kv[0], w.n_kv[1]);
   w.lo = item == share[0] ? share[1] : 0;
   const int hi = item == share[2] ? share[3] : n;
@@ -595,10 +595,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (args.sort_items) return k < *n_mine ? item_list[k] : -1;
     return snake_item(k, n_items);
   };
-  auto cta_work = [&](int item) -> Work {
-    Work w = decode_work<SPLIT>(args, item);
-    if (SPLIT && args.shares) clip_work(w, item, item_list);
-    return w;
+  using ItemWork = typename std::conditional<SPLIT, Piece, Work>::type;
+  auto cta_work = [&](int item) -> ItemWork {
+    if constexpr (SPLIT) {
+      Piece w;
+      static_cast<Work&>(w) = decode_work<true>(args, item);
+      w.lo = 0;
+      w.part = false;
+      if (args.shares) clip_work(w, item, item_list);
+      return w;
+    } else {
+      return decode_work(args, item);
+    }
   };
 
   if (warp >= SOFTMAX_WARPS) {
@@ -613,7 +621,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int nq = 0;          // items whose Q was loaded
       bool ok = true;
       for (int kk_item = 0, item; ok && (item = cta_item(kk_item)) >= 0; ++kk_item) {
-        const Work w = cta_work(item);
+        const ItemWork w = cta_work(item);
         const int n_kv = max(w.n_kv[0], w.n_kv[1]);
         if (!w.active[0] && !w.active[1]) continue;
         if (PAGED && args.seqlens_k[w.b] > args.max_blocks * 16 && args.error_flags)
@@ -704,7 +712,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // The tensor core consumes K_0, V_0, K_1, V_1, ...; each load first
         // waits for the block two back in its ring to be released.
         for (int i = 0; i < n_kv && ok; ++i) {
-          const int blk = SPLIT ? w.lo + i : i;
+          const int blk = first_block(w) + i;
           fetch_table(blk);
           ok = load(false, blk);
           if (ok) ok = load(true, blk);
@@ -769,7 +777,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int nq = 0;          // active items so far (Q phases)
       bool ok = true;
       for (int kk_item = 0, item; ok && (item = cta_item(kk_item)) >= 0; ++kk_item) {
-        const Work w = cta_work(item);
+        const ItemWork w = cta_work(item);
         if (!w.active[0] && !w.active[1]) continue;
         const int n_kv = max(w.n_kv[0], w.n_kv[1]);
         // S of block i for every tile that has it; then K_i can be released.
@@ -854,7 +862,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int nf = 0;  // items this tile finished (o_full phases)
     bool ok = true;
     for (int kk_item = 0, item; ok && (item = cta_item(kk_item)) >= 0; ++kk_item) {
-      const Work w = cta_work(item);
+      const ItemWork w = cta_work(item);
       if (!w.active[0] && !w.active[1]) continue;
       const int n_kv = max(w.n_kv[0], w.n_kv[1]);
       const int nt = w.n_kv[t];
@@ -866,7 +874,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // (tail slots of a partly filled cache block); they are zeroed in shared
       // memory before this tile's last P V, because 0 * NaN would poison O.
       const bool v_fix = PAGED && nt == n_kv && nt > 0 && (w.sk & 15) != 0 && nt * BK > w.sk;
-      const int qrow = w.row0[t] + r;
+      // SPLIT: this thread's row is one of several heads' (row_bits).
+      const int qrow = w.row0[t] + (SPLIT ? r & ((1 << args.row_bits) - 1) : r);
+      auto head = [&] { return SPLIT ? w.head[t] + (r >> args.row_bits) : w.head[t]; };
       const int qpos = qrow + (w.sk - w.sq);  // absolute position (bottom-right causal)
       float m2 = -INFINITY;  // running max of s * scale * log2(e)
       float l = 0.f;         // running sum of 2^(s*scale*log2e - m2)
@@ -883,7 +893,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float s[BK];
 #pragma unroll
         for (int c = 0; c < BK; ++c) s[c] = __uint_as_float(sb[c]);
-        const int k0 = (SPLIT ? w.lo + i : i) * BK;
+        const int k0 = (first_block(w) + i) * BK;
         const bool need_mask = (k0 + BK > w.sk) || (args.causal && (k0 + BK - 1 > w.row0[t] + (w.sk - w.sq)));
         if (need_mask) {
           const int lim = args.causal ? min(w.sk, qpos + 1) : w.sk;  // keys [0, lim) visible
@@ -966,17 +976,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // The row, head and batch coordinates of this row's O and LSE (rows
       // past the sequence end are not stored).
       const bool out_ok =
-          !store || ATTN_IN_BOUNDS(w.qoff + qrow >= 0 && w.qoff + qrow < args.out_rows && w.head[t] >= 0 &&
-                                       w.head[t] < args.hq && w.qb >= 0 && w.qb < (args.cu_seqlens_q ? 1 : args.batch),
+          !store || ATTN_IN_BOUNDS(w.qoff + qrow >= 0 && w.qoff + qrow < args.out_rows && head() >= 0 &&
+                                       head() < args.hq && w.qb >= 0 && w.qb < (args.cu_seqlens_q ? 1 : args.batch),
                                    ATTN_SITE_PREFILL_OUT, args.error_flags, args.planted);
       // A piece of an item: O (normalised) and LSE go to the CTA's slot of partial results.
-      const bool part = SPLIT && w.part;
-      const long long slot = part ? (2LL * blockIdx.x + (w.lo > 0 ? 0 : 1)) * 2 + t : 0;
+      const bool part = is_part(w);
+      const long long slot = part ? (2LL * blockIdx.x + (first_block(w) > 0 ? 0 : 1)) * 2 + t : 0;
       if (part) {
         if (store && out_ok) args.part_lse[slot * BM + r] = empty ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994530942f;
       } else if (args.lse && store && out_ok) {
         const float lse = empty ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994530942f;
-        args.lse[((long long)w.qb * args.hq + w.head[t]) * args.lse_rows + w.qoff + qrow] = lse;
+        args.lse[((long long)w.qb * args.hq + head()) * args.lse_rows + w.qoff + qrow] = lse;
       }
       const bool has_keys = nt > 0;
       if (has_keys) {
@@ -984,12 +994,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ++nf;
         if (!ok) break;
       }
-      const long long obase = (long long)w.qb * args.o_bs + (long long)w.head[t] * args.o_hs +
+      const long long obase = (long long)w.qb * args.o_bs + (long long)head() * args.o_hs +
                               (long long)(w.qoff + qrow) * args.o_rs;
       if (has_keys) tc_fence_after();
-      if (!part && args.o_tma && w.row0[t] + sub * 32 + 32 <= w.sq) {  // warp-uniform
+      // The warp's 32 rows are one head's (SPLIT: the host sees to it) and all there.
+      const int warp_row = w.row0[t] + (SPLIT ? (sub * 32) & ((1 << args.row_bits) - 1) : sub * 32);
+      if (!part && args.o_tma && warp_row + 32 <= w.sq) {  // warp-uniform
         uint8_t* stage = smem + L::O_OFF + warp * L::W_STAGE;
-        const int r0 = w.qoff + w.row0[t] + sub * 32;
+        const int r0 = w.qoff + warp_row;
         // The warp's staging area (one 4 KB box per round) and its 32 output
         // rows.
         if (ATTN_IN_BOUNDS(warp >= 0 && warp < SOFTMAX_WARPS &&
@@ -997,9 +1009,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                r0 >= 0 && r0 + 32 <= args.out_rows,
                            ATTN_SITE_PREFILL_SMEM_STAGE, args.error_flags, args.planted)) {
           if (args.o_f32)
-            store_rows_tma<D, true>(&tm_o, stage, tO, has_keys && o_cols, inv_l, r0, w.head[t], w.qb);
+            store_rows_tma<D, true>(&tm_o, stage, tO, has_keys && o_cols, inv_l, r0, head(), w.qb);
           else
-            store_rows_tma<D, false>(&tm_o, stage, tO, has_keys && o_cols, inv_l, r0, w.head[t], w.qb);
+            store_rows_tma<D, false>(&tm_o, stage, tO, has_keys && o_cols, inv_l, r0, head(), w.qb);
         }
         continue;
       }
@@ -1082,13 +1094,15 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) split_combine_kernel(const
   if (item < 0) return;
   const Work w = decode_work<true>(args, item);
   const int r0 = blockIdx.z * COMBINE_ROWS, r = r0 + lane;
-  const int rows = min(COMBINE_ROWS, w.sq - (w.row0[t] + r0));
-  if (!w.active[t] || rows <= 0) return;
+  auto qrow_of = [&](int row) { return w.row0[t] + (row & ((1 << args.row_bits) - 1)); };
+  auto head_of = [&](int row) { return w.head[t] + (row >> args.row_bits); };
+  const bool live = qrow_of(r) < w.sq;
+  if (!w.active[t] || __ballot_sync(0xffffffffu, live) == 0) return;  // the same rows in every warp
   float m = -INFINITY, sum = 0.f;
   float4 acc[GROUPS];
 #pragma unroll
   for (int k = 0; k < GROUPS; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (lane < rows) {
+  if (live) {
 #pragma unroll 2
     for (int i = 0; i < n; ++i) {
       // Piece i: the CTA's second slot, then the first slots of those behind it.
@@ -1117,16 +1131,16 @@ __global__ void __launch_bounds__(COMBINE_WARPS * 32) split_combine_kernel(const
   for (int k = 0; k < GROUPS; ++k)
     *reinterpret_cast<float4*>(&s_o[lane][(k * COMBINE_WARPS + warp_id()) * 4]) =
         make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
-  if (warp_id() == 0 && lane < rows && args.lse)
-    args.lse[((long long)w.qb * args.hq + w.head[t]) * args.lse_rows + w.qoff + w.row0[t] + r] =
+  if (warp_id() == 0 && live && args.lse)
+    args.lse[((long long)w.qb * args.hq + head_of(r)) * args.lse_rows + w.qoff + qrow_of(r)] =
         empty ? -INFINITY : m + log2f(sum) * LN2;
   __syncthreads();
-  const long long o0 = (long long)w.qb * args.o_bs + (long long)w.head[t] * args.o_hs +
-                       (long long)(w.qoff + w.row0[t] + r0) * args.o_rs;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += COMBINE_WARPS * 32) {
-    const int row = i / (D / 4), col = i % (D / 4) * 4;
+  for (int i = threadIdx.x; i < COMBINE_ROWS * (D / 4); i += COMBINE_WARPS * 32) {
+    const int row = i / (D / 4), col = i % (D / 4) * 4, qrow = qrow_of(r0 + row);
+    if (qrow >= w.sq) continue;
     const float4 x = *reinterpret_cast<const float4*>(&s_o[row][col]);
-    const long long o = o0 + row * args.o_rs + col;
+    const long long o = (long long)w.qb * args.o_bs + (long long)head_of(r0 + row) * args.o_hs +
+                        (long long)(w.qoff + qrow) * args.o_rs + col;
     if (args.o_f32)
       *reinterpret_cast<float4*>(reinterpret_cast<float*>(args.o) + o) = x;
     else
@@ -1158,14 +1172,15 @@ static EncodeTiledFn get_encode_fn() {
 }
 
 // 4-D map over [d3][d2][d1][d0 = head_dim] with byte strides s1..s3, box
-// (128 bytes of d0, box_rows, 1, 1), 128-byte swizzle, zero fill out of bounds.
+// (128 bytes of d0, box_rows, box_d2, 1), 128-byte swizzle, zero fill out of bounds.
 static bool encode_4d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t d3,
-                      uint64_t s1, uint64_t s2, uint64_t s3, uint32_t box_rows, bool f32 = false) {
+                      uint64_t s1, uint64_t s2, uint64_t s3, uint32_t box_rows, bool f32 = false,
+                      uint32_t box_d2 = 1) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[4] = {d0, d1, d2, d3};
   cuuint64_t strides[3] = {s1, s2, s3};
-  cuuint32_t box[4] = {f32 ? 32u : 64u, box_rows, 1, 1};
+  cuuint32_t box[4] = {f32 ? 32u : 64u, box_rows, box_d2, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                   const_cast<void*>(base), dims, strides, box, estr,
@@ -1245,8 +1260,22 @@ static long long prefill_items(const attn_prefill_params& p) {
   return group % 2 == 0 ? blocks * p.batch * p.num_kv_heads * (group / 2) : (blocks + 1) / 2 * p.batch * p.num_q_heads;
 }
 
+// SPLIT: a tile takes as many heads of a kv head as divide its group (up to 8, a
+// power of two) and so many fewer query rows of each, so that few or ragged
+// query rows leave little of it empty. log2 of the query rows:
+static int split_row_bits(const attn_prefill_params& p) {
+  const int group = p.num_q_heads / p.num_kv_heads;
+  return group % 8 == 0 ? 4 : group % 4 == 0 ? 5 : group % 2 == 0 ? 6 : 7;
+}
+
+long long prefill_split_items(const attn_prefill_params& p) {
+  const int bits = split_row_bits(p), heads = 128 >> bits;
+  const long long blocks = ((long long)p.seqlen_q + (2 << bits) - 1) >> (bits + 1);
+  return blocks * p.batch * (p.num_q_heads / heads);
+}
+
 static bool splits(const attn_prefill_params& p) {
-  return prefill_items(p) <= prefill::SORT_MAX_ITEMS && p.seqlen_k > prefill::SPLIT_MIN_KEYS;
+  return prefill_split_items(p) <= prefill::SORT_MAX_ITEMS && p.seqlen_k > prefill::SPLIT_MIN_KEYS;
 }
 
 size_t prefill_split_workspace_bytes(const attn_prefill_params& p) {
@@ -1269,8 +1298,9 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
   const int64_t q_bs = packed ? p.q_row_stride * (int64_t)p.total_q : p.q_batch_stride;
   const int64_t o_bs = packed ? p.o_row_stride * (int64_t)p.total_q : p.o_batch_stride;
   CUtensorMap tq, tk, tv;
+  const int row_bits = behind ? split_row_bits(p) : 7;
   if (!encode_4d(&tq, p.q, D, q_rows, p.num_q_heads, q_batches, p.q_row_stride * 2, p.q_head_stride * 2, q_bs * 2,
-                 BM))
+                 1 << row_bits, false, 128 >> row_bits))
     return ATTN_ERR_CUDA;
   if (paged) {
     // Pools [num_blocks, Hkv, 16, D]: one 16-row box per cache block and D chunk.
@@ -1300,14 +1330,13 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
   a.scale_log2 = p.scale * 1.4426950408889634f;
   a.causal = p.causal ? 1 : 0;
   a.pair_heads = (a.group % 2 == 0) ? 1 : 0;
-  if (behind && a.pair_heads) {
-    a.fd_outer.init((p.seqlen_q + BM - 1) / BM * (a.group / 2));
-    a.fd_mid.init(a.group / 2);
+  a.row_bits = row_bits;
+  if (behind) {
+    const int blocks = (int)(((long long)p.seqlen_q + (2 << row_bits) - 1) >> (row_bits + 1));
+    const int sets = a.group >> (7 - row_bits);
+    a.fd_outer.init(blocks * sets);
+    a.fd_mid.init(sets);
     a.fd_inner.init(p.num_kv_heads);
-  } else if (behind) {
-    a.fd_outer.init(((p.seqlen_q + BM - 1) / BM + 1) / 2);
-    a.fd_mid.init(p.num_q_heads);
-    a.fd_inner.init(a.group);
   } else if (a.pair_heads) {
     a.fd_outer.init(p.batch * p.num_kv_heads * (a.group / 2));
     a.fd_mid.init(a.group / 2);
@@ -1317,7 +1346,8 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
     a.fd_mid.init(p.num_q_heads);
     a.fd_inner.init(a.group);
   }
-  a.n_row_blocks = (p.seqlen_q + BM - 1) / BM;
+  a.n_row_blocks = behind ? (int)(((long long)p.seqlen_q + (2 << row_bits) - 1) >> (row_bits + 1))
+                          : (p.seqlen_q + BM - 1) / BM;
   a.seqlens_q = p.seqlens_q;
   a.seqlens_k = p.seqlens_k;
   a.cu_seqlens_q = p.cu_seqlens_q;
@@ -1337,6 +1367,7 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
                       o_bs * esz, 32, a.o_f32 != 0)
                 ? 1
                 : 0;
+  if (row_bits < 5) a.o_tma = 0;  // a warp's rows are two heads'
   if (!a.o_tma) to = tq;  // never read
   a.error_flags = p.error_flags;
   a.wait_limit = pipeline_wait_limit();
@@ -1347,7 +1378,7 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
     a.max_blocks = p.max_blocks_per_seq;
     a.num_blocks = p.num_blocks;
   }
-  const long long items = prefill_items(p);
+  const long long items = behind ? prefill_split_items(p) : prefill_items(p);
   if (items <= 0) return ATTN_OK;
   if (items > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
 
