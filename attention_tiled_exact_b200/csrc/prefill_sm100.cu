@@ -301,8 +301,8 @@ __device__ void order_items(const Args& a, int n_items, unsigned long long* keys
 
 // SPLIT: the items' key blocks are dealt out evenly, cut where a CTA's share
 // ends, so that a few long items (or one) fill the machine as well as many.
-// An item costs its key blocks plus a fixed 11/8 of a block (as in
-// order_items); CTA c takes the c-th of gridDim.x equal parts of the items' total in
+// An item costs its key blocks plus a fixed 19/8 of a block (11/8, which is its
+// cost where no piece goes through memory, left 1-5 % more time); CTA c takes the c-th of gridDim.x equal parts of the items' total in
 // item order. Every CTA computes all costs (scratch: the K ring) and finds its
 // two boundaries, each an item and the first block behind it: share[] = first
 // item and block, last item and block (excluded), number of items touched.
@@ -312,7 +312,8 @@ __device__ void order_items(const Args& a, int n_items, unsigned long long* keys
 // CTAs of one item follow one another: inside an item a share is at least a
 // block, because it is MIN_SHARE of cost at least.
 constexpr int SPLIT_MIN_KEYS = 4 * BK;  // up to this bound of the keys an item is not worth cutting
-constexpr int MIN_SHARE = 16;  // eighths of a block: a CTA without 2 blocks' worth gets none
+constexpr int PIECE_COST = 19;  // eighths of a block
+constexpr int MIN_SHARE = 16;   // eighths of a block: a CTA without 2 blocks' worth gets none
 template <int NT>
 __device__ void split_items(const Args& a, int n_items, int* cost, int* share) {
   long long* sums = reinterpret_cast<long long*>(cost + SORT_MAX_ITEMS);
@@ -321,7 +322,7 @@ __device__ void split_items(const Args& a, int n_items, int* cost, int* share) {
   long long mine = 0;
   for (int i = i0; i < i1; ++i) {
     const Work w = decode_work<true>(a, i);
-    cost[i] = (w.active[0] || w.active[1]) ? max(w.n_kv[0], w.n_kv[1]) * 8 + 11 : 0;
+    cost[i] = (w.active[0] || w.active[1]) ? max(w.n_kv[0], w.n_kv[1]) * 8 + PIECE_COST : 0;
     mine += cost[i];
   }
   long long before = mine;  // inclusive sum over the warp, then exclusive over the block
@@ -351,7 +352,7 @@ __device__ void split_items(const Args& a, int n_items, int* cost, int* share) {
     long long p = before;
     for (int i = i0; i < i1; p += cost[i], ++i) {
       if (x < p || x >= p + cost[i]) continue;
-      const int off = (int)(x - p), n = (cost[i] - 11) / 8;
+      const int off = (int)(x - p), n = (cost[i] - PIECE_COST) / 8;
       const int blk = off <= 8 ? 0 : min(n, (off - 4) / 8);
       share[2 * e] = blk > 0 && blk == n ? i + 1 : i;
       share[2 * e + 1] = blk == n ? 0 : blk;
