@@ -774,29 +774,31 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     """
     index = _device_index(seq_lens, new_lens, block_table, free_blocks, num_used, seq_lens_out, cu_seqlens_q,
                           positions, slot_map, num_used_out, error_flags)
-    B, total_q = seq_lens.numel(), int(total_q)
+    B, total_q, num_free = seq_lens.numel(), int(total_q), free_blocks.numel()
     if total_q < 0:
         raise ValueError("total_q >= 0")
-    columns, num_free = _table(block_table, B), free_blocks.numel()
-    _i32_vec(free_blocks, num_free, "free_blocks")
-    _i32_vec(seq_lens, B, "seq_lens")
+    columns = _table(block_table, B)
+    dev = None
+    if seq_lens_out is None or cu_seqlens_q is None or positions is None or slot_map is None or num_used_out is None:
+        dev = seq_lens.device
     if seq_lens_out is None:
-        seq_lens_out = torch.empty(B, dtype=_I32, device=seq_lens.device)
+        seq_lens_out = torch.empty(B, dtype=_I32, device=dev)
     if cu_seqlens_q is None:
-        cu_seqlens_q = torch.empty(B + 1, dtype=_I32, device=seq_lens.device)
+        cu_seqlens_q = torch.empty(B + 1, dtype=_I32, device=dev)
     if positions is None:
-        positions = torch.empty(total_q, dtype=_I32, device=seq_lens.device)
+        positions = torch.empty(total_q, dtype=_I32, device=dev)
     if slot_map is None:
-        slot_map = torch.empty(total_q, dtype=_I32, device=seq_lens.device)
+        slot_map = torch.empty(total_q, dtype=_I32, device=dev)
     if num_used_out is None:
-        num_used_out = torch.empty(1, dtype=_I32, device=seq_lens.device)
-    _i32_vec(new_lens, B, "new_lens")
-    _i32_vec(num_used, 1, "num_used")
-    _i32_vec(seq_lens_out, B, "seq_lens_out")
-    _i32_vec(cu_seqlens_q, B + 1, "cu_seqlens_q")
-    _i32_vec(positions, total_q, "positions")
-    _i32_vec(slot_map, total_q, "slot_map")
-    _i32_vec(num_used_out, 1, "num_used_out")
+        num_used_out = torch.empty(1, dtype=_I32, device=dev)
+    if new_lens.numel() != B or seq_lens_out.numel() != B or cu_seqlens_q.numel() != B + 1 or \
+            positions.numel() != total_q or slot_map.numel() != total_q or num_used.numel() != 1 or \
+            num_used_out.numel() != 1:
+        raise ValueError("sizes: new_lens, seq_lens_out [B], cu_seqlens_q [B + 1], positions, slot_map [total_q], "
+                         "num_used, num_used_out [1]")
+    for t in (seq_lens, new_lens, free_blocks, num_used, seq_lens_out, cu_seqlens_q, positions, slot_map, num_used_out):
+        if t.dtype is not _I32 or not t.is_contiguous():
+            raise ValueError("contiguous int32 tensors")
     p = _pack_plan(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
                    num_used.data_ptr(), seq_lens_out.data_ptr(), cu_seqlens_q.data_ptr(), positions.data_ptr(),
                    slot_map.data_ptr(), num_used_out.data_ptr(), _opt(error_flags), B, columns, int(num_blocks),

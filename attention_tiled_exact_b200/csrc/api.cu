@@ -64,10 +64,16 @@ int device_sm_count() {
 }
 
 attn_status_t check_device() {
+  static std::atomic<int> known[kMaxDevices] = {};  // 0: not asked yet, 1: sm_100, 2: another device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return ATTN_ERR_NO_DEVICE;
+  }
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (cached) {
+    const int k = known[dev].load(std::memory_order_relaxed);
+    if (k != 0) return k == 1 ? ATTN_OK : ATTN_ERR_NO_DEVICE;
   }
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -75,7 +81,9 @@ attn_status_t check_device() {
     cudaGetLastError();
     return ATTN_ERR_NO_DEVICE;
   }
-  return (major == 10 && minor == 0) ? ATTN_OK : ATTN_ERR_NO_DEVICE;
+  const bool ok = major == 10 && minor == 0;
+  if (cached) known[dev].store(ok ? 1 : 2, std::memory_order_relaxed);
+  return ok ? ATTN_OK : ATTN_ERR_NO_DEVICE;
 }
 
 attn_status_t validate_prefill(const attn_prefill_params* p) {
