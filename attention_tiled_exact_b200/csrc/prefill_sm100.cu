@@ -1295,6 +1295,9 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
   if (p.batch == 0 || p.seqlen_q == 0 || p.num_q_heads == 0) return ATTN_OK;
   const bool paged = p.k_cache != nullptr;
   const int D = p.head_dim;
+  const long long items = behind ? prefill_split_items(p) : prefill_items(p);
+  if (items <= 0) return ATTN_OK;
+  if (items > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
   // Packed queries ([total_q, Hq, D] rows addressed through cu_seqlens_q) are
   // one "batch" of total_q rows to the tensor maps.
   const bool packed = p.cu_seqlens_q != nullptr;
@@ -1383,9 +1386,6 @@ static attn_status_t launch_prefill_with(const attn_prefill_params& p, cudaStrea
     a.max_blocks = p.max_blocks_per_seq;
     a.num_blocks = p.num_blocks;
   }
-  const long long items = behind ? prefill_split_items(p) : prefill_items(p);
-  if (items <= 0) return ATTN_OK;
-  if (items > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
 
   // A quarter of the exponentials go to the FMA-pipe polynomial (measured best
   // on B200 for head_dim 128: the MUFU pipe is the scarcer resource).

@@ -544,37 +544,56 @@ def test_prefill_block_scaled_bounds_and_empty_rows(lib):
     # no keys at all
     o, lse = lib.prefill_paged_block_scaled(q, *dev, _i32([0, 0]).cuda(), max_seqlen_k=0)
     assert (o == 0).all() and torch.isneginf(lse).all()
+    # the same for as many rows and keys as the tensor-core tiles are taken for
+    c = _decode_case([900, 500], 16, 2, 128, 25)
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
+    q = torch.randn(2, 16, 600, 128, generator=_gen(26)).to(torch.bfloat16).cuda()
+    flags.zero_()
+    o, lse = lib.prefill_paged_block_scaled(q, *dev, _i32([900, 500]).cuda(), max_seqlen_k=900, error_flags=flags)
+    assert (o[1, :, :100] == 0).all() and torch.isneginf(lse[1, :, :100]).all() and torch.isfinite(lse[1, :, 100:]).all()
+    assert torch.isfinite(o).all() and int(flags.item()) == 0
+    o2, _ = lib.prefill_paged_block_scaled(q, *dev, _i32([900, -4]).cuda(), max_seqlen_k=833, causal=False, error_flags=flags)
+    o3, _ = lib.prefill_paged_block_scaled(q, *dev, _i32([833, 0]).cuda(), max_seqlen_k=833, causal=False)
+    assert int(flags.item()) == lib.ATTN_FAULT_BAD_LENGTH and torch.equal(o2, o3) and (o2[1] == 0).all()
+    dev[4][0, 3] = 10 ** 6  # a page outside the pool: flagged, read as zeros
+    o, _ = lib.prefill_paged_block_scaled(q, *dev, _i32([900, 500]).cuda(), max_seqlen_k=900, error_flags=flags)
+    assert int(flags.item()) & lib.ATTN_FAULT_BAD_BLOCK and torch.isfinite(o).all()
 
 
 @gpu
-@pytest.mark.parametrize("context", [20, 1500])
-def test_prefill_block_scaled_nan_in_a_visible_key(lib, context):
-    """Rows that see a NaN key give NaN (O and LSE), the rows before it and the other head do not."""
-    n, rows = context + 9, 9
+@pytest.mark.parametrize("rows,context,D,Hq", [(9, 20, 64, 4), (9, 1500, 64, 4), (512, 2000, 128, 8)])
+def test_prefill_block_scaled_nan_in_a_visible_key(lib, rows, context, D, Hq):
+    """Rows that see a NaN key give NaN (O and LSE), the rows before it and the other head do not.
+
+    The last case has the rows and keys for which the tensor-core tiles are taken."""
+    n, G = context + rows, Hq // 2
     for col in range(8):  # every place in a run of columns
-        c = _decode_case([n], 4, 2, 64, 22)
+        c = _decode_case([n], Hq, 2, D, 22)
         at = context + 1 + col % 8
         c["kc"][int(c["table"][0, at // 16]), 1, at % 16, 3] = 0x7F
         dev = [c[k].cuda() for k in ("kc", "vc", "ks", "vs", "table")]
-        q = torch.randn(1, 4, rows, 64, generator=_gen(col)).to(torch.bfloat16).cuda()
+        q = torch.randn(1, Hq, rows, D, generator=_gen(col)).to(torch.bfloat16).cuda()
         o, lse = lib.prefill_paged_block_scaled(q, *dev, _i32([n]).cuda(), max_seqlen_k=n)
         sees = torch.arange(context, n) >= at
-        assert torch.isfinite(o[:, :2]).all() and torch.isfinite(lse[:, :2]).all()
-        for h in (2, 3):
+        assert torch.isfinite(o[:, :G]).all() and torch.isfinite(lse[:, :G]).all()
+        for h in range(G, Hq):
             assert torch.equal(torch.isnan(o[0, h]).all(-1).cpu(), sees) and torch.equal(torch.isnan(lse[0, h]).cpu(), sees)
             assert torch.isfinite(o[0, h][~sees]).all()
 
 
 @gpu
-@pytest.mark.parametrize("Hq,Hk", [(4, 2), (3, 1)])
-def test_prefill_block_scaled_shared_items(lib, Hq, Hk):
-    """Few rows over long keys: every item's keys are shared by many CTAs, and ragged lengths end inside shares."""
-    D, chunks, lens = 64, [1, 130, 3, 0], [6000, 4100, 3, 900]
+@pytest.mark.parametrize("D,Hq,Hk,chunks", [(64, 4, 2, [1, 130, 3, 0]), (128, 8, 2, [300, 1, 77, 0]),
+                                            (128, 3, 1, [300, 1, 77, 0]), (128, 16, 2, [40, 300, 3, 0]),
+                                            (64, 24, 2, [300, 1, 3, 200])])
+def test_prefill_block_scaled_shared_items(lib, D, Hq, Hk, chunks):
+    """Chunks over long keys (all but the first for the tensor-core tiles, with 4, 1, 8 and 4 heads per tile): every
+    item's keys are shared by many CTAs, and ragged lengths end inside shares."""
+    lens = [6000, 4100, max(3, chunks[2]), 900]
     c = _decode_case(lens, Hq, Hk, D, 23)
     q = torch.randn(sum(chunks), Hq, D, generator=_gen(24)).to(torch.bfloat16)
-    cu = [0, 1, 131, 134, 134]
+    cu = [0] + torch.cumsum(torch.tensor(chunks), 0).tolist()
     dev = [c[k].cuda() for k in ("kc", "vc", "ks", "vs", "table")]
-    runs = [lib.prefill_paged_block_scaled(q.cuda(), *dev, _i32(lens).cuda(), cu_seqlens_q=_i32(cu).cuda(), max_seqlen_q=130,
+    runs = [lib.prefill_paged_block_scaled(q.cuda(), *dev, _i32(lens).cuda(), cu_seqlens_q=_i32(cu).cuda(), max_seqlen_q=max(chunks),
                                            out_dtype=torch.float32) for _ in range(2)]
     assert torch.equal(runs[0][0], runs[1][0]) and torch.equal(runs[0][1], runs[1][1])  # no order of arrival in it
     kv, vv = ref.values(c["kc"], c["ks"]), ref.values(c["vc"], c["vs"])
@@ -615,7 +634,7 @@ def test_offsets_past_32_bits(lib):
         k, v = lib.gather_paged(pools[0], pools[1], table, lens, new, *scales)
         o, lse = lib.decode_paged_block_scaled(q[-1:].contiguous(), *args, table, lens)
         p, _ = lib.prefill_paged_block_scaled(q, *args, table, lens, cu_seqlens_q=_i32([0, new]).cuda(), max_seqlen_q=new)
-        big = qkv.new_zeros(1, 4 * Hq, 512, D)  # many rows: the tensor-core path
+        big = qkv.new_zeros(1, 4 * Hq, 1024, D)  # many rows: the tensor-core path
         t, _ = lib.prefill_paged_block_scaled(big, *args, table, lens, causal=False)
         outs.append((q, k, v, o, lse, p, t))
     for a, b in zip(*outs):
@@ -644,9 +663,9 @@ def test_empty_calls(lib):
 
 
 @gpu
-@pytest.mark.parametrize("chunk", [2, 200])
+@pytest.mark.parametrize("chunk", [2, 600])
 def test_rows_behind_the_last_sequence_are_left_alone(lib, chunk):
-    c = _decode_case([700, 300], 8, 2, 128, 42)
+    c = _decode_case([700, 650], 8, 2, 128, 42)
     dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
     q = torch.randn(2 * chunk + 5, 8, 128, generator=_gen(1)).to(torch.bfloat16).cuda()
     out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
@@ -713,11 +732,11 @@ from tests import test_paged_cache as t
 assert lib.debug_bounds_enabled()
 for splits in (0, 1, 16):
     assert t._decode_run(lib, t._decode_case([1, 0, 2500, 300], 9, 3, 128, 1), num_splits=splits)[2] == 0
-c = t._decode_case([900, 40], 4, 2, 64, 2)
+c = t._decode_case([900, 640], 16, 2, 128, 2)
 dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
-for rows in (3, 400):
+for rows in (3, 600):
     flags = torch.zeros(1, dtype=torch.int32, device="cuda")
-    q = torch.zeros(2, 4, rows, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(2, 16, rows, 128, dtype=torch.bfloat16, device="cuda")
     lib.prefill_paged_block_scaled(q, *dev, t._i32(c["lens"]).cuda(), error_flags=flags)
     assert int(flags.item()) == 0
 print("clean")
