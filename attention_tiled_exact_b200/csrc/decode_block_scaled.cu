@@ -41,7 +41,9 @@
 // Bound by HBM for full batches (64 sequences of 1K to 32K tokens, 32/8 heads of
 // 128: 324-335 us, 6.5-6.7 TB/s; the other order of the products, with a maximum
 // per block, took 384 us) and by its chain of length, table, pages, products and
-// merge for few: one sequence of 4097 tokens 10.6 us, 8 of 4096 17 us (66 MB).
+// merge for few: one sequence of 4097 tokens 9.1 us, 8 of 4096 17 us (66 MB). The
+// CTAs of a cluster read one another's results: sending them to the CTA that
+// merges them, ahead of one barrier instead of two, took 0.7 us longer.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -62,13 +64,13 @@ namespace bsdecode {
 namespace cg = cooperative_groups;
 
 constexpr int BS = 16;
-constexpr int WARPS = 4;
-constexpr int THREADS = WARPS * 32;
+constexpr int COMBINE_WARPS = 4;
 constexpr int STAGES = 3;
 constexpr int CLUSTER = 8;      // CTAs that merge through shared memory, at most
 // Cache blocks: the least that a CTA is started for (2 per warp), the least per
 // CTA of a row of several clusters, and the pieces of a grid of many rounds.
 constexpr int MIN_BLOCKS = 8, LONG_BLOCKS = 32, EVEN_BLOCKS = 256;
+constexpr int WIDE_CTAS = 1;  // CTAs per SM up to which they have 8 warps
 constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units
 constexpr float LN2 = 0.69314718055994530942f;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -97,16 +99,16 @@ struct Args {
   int planted;
 };
 
-// CTAs per SM that the kernels are built for.
+// CTAs of 4 warps per SM that the kernels are built for; half as many of 8.
 template <int D, int HALVES>
 constexpr int ctas_per_sm() {
   return HALVES == 2 ? 3 : D == 128 ? 4 : 5;
 }
-template <int D>
+template <int D, int WARPS>
 struct Ring {
   uint8_t kv[WARPS][STAGES][2][BS * D];
 };
-template <int D, int ROWS>
+template <int D, int ROWS, int WARPS>
 struct Merge {  // over the ring, when it is empty
   float m[WARPS][ROWS], r[WARPS][ROWS], l[WARPS][ROWS];
   float o[WARPS][ROWS][D];
@@ -114,9 +116,10 @@ struct Merge {  // over the ring, when it is empty
   float cta_m[ROWS], cta_r[ROWS], cta_l[ROWS];
   float cta_o[ROWS][D];
 };
-template <int D, int ROWS>
+template <int D, int ROWS, int WARPS>
 constexpr int smem_bytes() {
-  return (int)(sizeof(Ring<D>) > sizeof(Merge<D, ROWS>) ? sizeof(Ring<D>) : sizeof(Merge<D, ROWS>));
+  constexpr int ring = (int)sizeof(Ring<D, WARPS>), merge = (int)sizeof(Merge<D, ROWS, WARPS>);
+  return ring > merge ? ring : merge;
 }
 
 // Byte offset of 16-byte chunk c of token `row` in a ring slot.
@@ -174,7 +177,7 @@ struct Group {
   int per_cta, used;  // of them for a CTA of the row of the grid, and CTAs that have some
 };
 
-template <int ROWS>
+template <int ROWS, int WARPS>
 __device__ __forceinline__ Group group_of(const Args& a, int gi, int ctas) {
   Group g;
   g.b = a.tiles == 1 ? gi : gi / a.tiles;
@@ -231,17 +234,17 @@ __device__ __forceinline__ float finish_row(float M, float R, float sum, float4&
 // CTAs of a cluster: the row of the grid up to CLUSTER.
 __device__ __forceinline__ int cluster_size() { return min((int)gridDim.x, CLUSTER); }
 
-template <int D, int HALVES, bool CLUSTERED>
-__global__ void __launch_bounds__(THREADS, ctas_per_sm<D, HALVES>()) few_rows_kernel(const Args a) {
-  constexpr int ROWS = 8 * HALVES;
+template <int D, int HALVES, bool CLUSTERED, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, ctas_per_sm<D, HALVES>() * 4 / WARPS) few_rows_kernel(const Args a) {
+  constexpr int ROWS = 8 * HALVES, THREADS = 32 * WARPS;
   constexpr int KSTEPS = D / 16, MT = D / 16;
   constexpr int COPIES = BS * D / (16 * 32);  // 16-byte copies per lane and block
   extern __shared__ __align__(128) uint8_t smem[];
-  Ring<D>& ring = *reinterpret_cast<Ring<D>*>(smem);
+  Ring<D, WARPS>& ring = *reinterpret_cast<Ring<D, WARPS>*>(smem);
   const int warp = warp_id(), lane = lane_id();
   const int gq = lane >> 2, tq = lane & 3;
   const int split = blockIdx.x, kvh = blockIdx.y;
-  const Group grp = group_of<ROWS>(a, blockIdx.z, gridDim.x);
+  const Group grp = group_of<ROWS, WARPS>(a, blockIdx.z, gridDim.x);
   const int b = grp.b;
   if (split == 0 && kvh == 0 && threadIdx.x == 0 && a.error_flags &&
       (unsigned)__ldg(a.seq_lens + b) > (unsigned)a.max_len)
@@ -489,7 +492,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<D, HALVES>()) few_rows_ke
 
   // ---- merge the warps
   __syncthreads();  // the ring becomes the merge buffer
-  Merge<D, ROWS>& mg = *reinterpret_cast<Merge<D, ROWS>*>(smem);
+  Merge<D, ROWS, WARPS>& mg = *reinterpret_cast<Merge<D, ROWS, WARPS>*>(smem);
 #pragma unroll
   for (int h = 0; h < HALVES; ++h)
 #pragma unroll
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<D, HALVES>()) few_rows_ke
         l[c] = 0.f;
         o[c] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c < n) {
-          const Merge<D, ROWS>& of = *cluster.map_shared_rank(&mg, c);
+          const Merge<D, ROWS, WARPS>& of = *cluster.map_shared_rank(&mg, c);
           m[c] = of.cta_m[row], r[c] = of.cta_r[row], l[c] = of.cta_l[row];
           o[c] = *reinterpret_cast<const float4*>(&of.cta_o[row][d]);
         }
@@ -575,31 +578,31 @@ __global__ void __launch_bounds__(THREADS, ctas_per_sm<D, HALVES>()) few_rows_ke
 // Merges the clusters' partial results of one row (blockIdx.x) of one tile and kv
 // head: O = sum_s e^(lse_s - lse) O_s, dealt out to 4 warps. A dependent launch:
 // it is set up while the last splits run.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int ctas) {
+template <int D, int ROWS, int SPLIT_WARPS>
+__global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const Args a, int ctas) {
   constexpr int PER = D / 32;
-  __shared__ float s_m[WARPS], s_sum[WARPS];
-  __shared__ __align__(16) float s_acc[WARPS][D];
+  __shared__ float s_m[COMBINE_WARPS], s_sum[COMBINE_WARPS];
+  __shared__ __align__(16) float s_acc[COMBINE_WARPS][D];
   const int row = blockIdx.x, kvh = blockIdx.y, warp = warp_id(), lane = lane_id();
-  const Group grp = group_of<ROWS>(a, blockIdx.z, ctas);
+  const Group grp = group_of<ROWS, SPLIT_WARPS>(a, blockIdx.z, ctas);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (row >= grp.rows || grp.used <= CLUSTER) return;
   const int n = (grp.used + CLUSTER - 1) / CLUSTER;
   const long long first = ((long long)blockIdx.z * a.hkv + kvh) * ROWS + row, step = (long long)gridDim.z * a.hkv * ROWS;
   float M = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += THREADS) M = fmaxf(M, __ldcg(a.part_lse + first + i * step));
+  for (int i = threadIdx.x; i < n; i += 32 * COMBINE_WARPS) M = fmaxf(M, __ldcg(a.part_lse + first + i * step));
 #pragma unroll
   for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, d));
   if (lane == 0) s_m[warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, s_m[w]);
+  for (int w = 0; w < COMBINE_WARPS; ++w) M = fmaxf(M, s_m[w]);
   const float Ms = M == -INFINITY ? 0.f : M;
   float sum = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll 4
-  for (int i = warp; i < n; i += WARPS) {
+  for (int i = warp; i < n; i += COMBINE_WARPS) {
     if (!ATTN_IN_BOUNDS(i < ctas / CLUSTER, ATTN_SITE_COMBINE, a.error_flags, a.planted)) break;
     const float w = ex2_approx((__ldcg(a.part_lse + first + i * step) - Ms) * LOG2E);
     const float* src = a.part_o + (first + i * step) * D + lane * PER;
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int ctas
   sum = 0.f;
   float4 out = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
+  for (int w = 0; w < COMBINE_WARPS; ++w) {
     sum += s_sum[w];
     add_scaled(out, 1.f, *reinterpret_cast<const float4*>(&s_acc[w][d]));
   }
@@ -641,7 +644,7 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const Args a, int ctas
 // (64 sequences of 1K to 32K tokens, 512 tiles: 8 CTAs 325 us, 4 CTAs 333 us,
 // 1 CTA 470 us, 16 CTAs 364 us). A row of more than one cluster costs a merge through
 // memory and is taken for LONG_BLOCKS per CTA (one sequence of 32768 tokens
-// and one kv head: 64 CTAs 12 us, 8 CTAs 45 us).
+// and one kv head: 64 CTAs 11 us, 8 CTAs 45 us).
 static int ctas_per_tile(const Args& a, int num_splits, int slots) {
   const long long blocks = (a.max_len + BS - 1) / BS, tiles = (long long)a.batch * a.tiles * a.hkv;
   long long n = num_splits;
@@ -656,10 +659,10 @@ static int ctas_per_tile(const Args& a, int num_splits, int slots) {
   return n >= 8 ? 8 : n >= 4 ? 4 : n >= 2 ? 2 : 1;
 }
 
-template <int D, int HALVES, bool CLUSTERED>
+template <int D, int HALVES, bool CLUSTERED, int WARPS>
 static attn_status_t launch_grid(const Args& a, int ctas, cudaStream_t stream) {
-  constexpr int ROWS = 8 * HALVES, SMEM = smem_bytes<D, ROWS>();
-  auto kern = few_rows_kernel<D, HALVES, CLUSTERED>;
+  constexpr int ROWS = 8 * HALVES, SMEM = smem_bytes<D, ROWS, WARPS>();
+  auto kern = few_rows_kernel<D, HALVES, CLUSTERED, WARPS>;
   static DeviceOnce setup;
   const attn_status_t st = setup.run([&]() -> attn_status_t {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
@@ -675,7 +678,7 @@ static attn_status_t launch_grid(const Args& a, int ctas, cudaStream_t stream) {
   attr[0].val.clusterDim.x = ctas < CLUSTER ? ctas : CLUSTER;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(ctas, a.hkv, a.batch * a.tiles);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -686,8 +689,9 @@ static attn_status_t launch_grid(const Args& a, int ctas, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     const long long rows = (long long)a.max_q * a.group;
     cfg.gridDim = dim3(rows < ROWS ? (int)rows : ROWS, a.hkv, a.batch * a.tiles);
+    cfg.blockDim = dim3(32 * COMBINE_WARPS);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, combine_kernel<D, ROWS>, a, ctas);
+    e = cudaLaunchKernelEx(&cfg, combine_kernel<D, ROWS, WARPS>, a, ctas);
   }
   if (e == cudaSuccess) return ATTN_OK;
   cudaGetLastError();
@@ -699,7 +703,7 @@ template <int D, int HALVES>
 static attn_status_t launch(Args a, int num_splits, void* workspace, size_t* bytes, cudaStream_t stream) {
   constexpr int ROWS = 8 * HALVES;
   a.tiles = (int)(((long long)a.max_q * a.group + ROWS - 1) / ROWS);
-  const int ctas = ctas_per_tile(a, num_splits, device_sm_count() * ctas_per_sm<D, HALVES>());
+  const int sms = device_sm_count(), ctas = ctas_per_tile(a, num_splits, sms * ctas_per_sm<D, HALVES>());
   const size_t n = ctas > CLUSTER ? (size_t)(ctas / CLUSTER) * a.batch * a.tiles * a.hkv * ROWS : 0;
   const size_t lse_at = n * D * sizeof(float);
   if (bytes) {
@@ -708,7 +712,13 @@ static attn_status_t launch(Args a, int num_splits, void* workspace, size_t* byt
   }
   a.part_o = reinterpret_cast<float*>(workspace);
   a.part_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + lse_at);
-  return ctas > 1 ? launch_grid<D, HALVES, true>(a, ctas, stream) : launch_grid<D, HALVES, false>(a, ctas, stream);
+  if (ctas == 1) return launch_grid<D, HALVES, false, 4>(a, ctas, stream);
+  // A warp's blocks follow one another, 0.6 us each, so a grid that leaves SMs
+  // empty deals a CTA's blocks to 8 warps: one sequence of 4097 tokens, 32/8 heads,
+  // 9.1 us (4 warps 10.3), of 32768 tokens, 8/1 heads, 11.3 us (12.5). Fuller
+  // grids measure alike with either (b = 8, 4096 tokens: 17 us).
+  const bool wide = (long long)ctas * a.batch * a.tiles * a.hkv <= WIDE_CTAS * (long long)sms;
+  return wide ? launch_grid<D, HALVES, true, 8>(a, ctas, stream) : launch_grid<D, HALVES, true, 4>(a, ctas, stream);
 }
 
 // Launches, or with `bytes` only gives the workspace's size.

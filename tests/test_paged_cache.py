@@ -413,6 +413,20 @@ def test_decode_block_scaled_matches_definition(lib, D, G, num_splits):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("batch,num_splits", [(2, 4), (2, 16), (40, 2), (40, 8), (6, 32)])
+def test_decode_block_scaled_small_and_large_grids(lib, D, G, batch, num_splits):
+    """Grids below one CTA per SM and above it, as one cluster and as several, with and without keys for every CTA."""
+    c = _decode_case(([4200, 130, 700, 1, 0, 257] + [40 + 31 * i for i in range(34)])[:batch], 2 * G, 2, D, 300 + G)
+    o, lse, tol, ltol = _decode_want(c)
+    go, gl, flags = _decode_run(lib, c, num_splits=num_splits, out_dtype=torch.float32, max_seq_len=max(c["lens"]))
+    assert flags == 0
+    _within(go, o, tol + 2.0 ** -21 * o.abs(), "O")
+    _within(gl, lse, ltol, "LSE")
+
+
+@gpu
 @pytest.mark.parametrize("spread", [0.0, 30.0])
 def test_decode_block_scaled_far_scales(lib, spread):
     """Blocks whose value scales lie up to 2^60 apart, keys near one scale; and a long sequence (many batches of blocks)."""
