@@ -1,10 +1,12 @@
 // Writing the paged cache (attn_append_paged) and reading it back
 // (attn_gather_paged), for sm_100a.
 //
-// Append, one launch with two kinds of CTAs. The first ones turn the query rows
-// (turn_rows). The others own a window of rows and a few kv heads: they find the
+// Append, one launch with two kinds of CTAs. The last ones turn the query rows
+// (turn_rows); behind the others, whose chain of loads is longer, they fill the
+// time that those wait (2048 rows of 32/8 heads 8.8 us, in front of them 11 us).
+// The others own a window of rows and some of the K and V heads: they find the
 // runs of consecutive slots that start in the window, compute the angles of the
-// runs' rows once for all heads, and two warps handle a run (at most 16 tokens,
+// runs' rows once for all K heads, and two warps handle a run (at most 16 tokens,
 // one cache block) of one head of K or V as a whole. A lane holds one 16-element
 // unit of 16 * units / 64 of the block's tokens in registers: kept tokens (in
 // front of the run) are read back as values, new ones are read and turned; one
@@ -16,8 +18,8 @@
 //   from the fp32 turned key, not from a bf16 copy of it.
 //
 // Both kernels read and write each element once. 8504 rows of 32/8 heads of 128:
-// append 44 us (191 MB; the queries alone 24 us at 5.8 TB/s, the keys and values
-// alone 20 us, where a run's load, reduction and store follow one another),
+// append 40 us (191 MB; the queries alone 23 us at 6.0 TB/s, the keys and values
+// alone 19 us, where a run's load, reduction and store follow one another),
 // gather 14 us (93 MB, 6.6 TB/s). A decode step of 32 rows takes 4.3 us and 3.7 us:
 // the launch and two dependent loads (slot, then row or block).
 #include <cuda_bf16.h>
@@ -42,7 +44,7 @@ constexpr unsigned FULL = 0xffffffffu;
 struct Append {
   rotary::Rows rows;  // the queries (rows.heads == 0: none)
   rotary::Turn turn;  // rotary_dim 0: nothing is turned
-  int q_blocks;       // blocks of the grid that turn queries
+  int kv_blocks;      // blocks of the grid in front of those that turn queries
   const __nv_bfloat16* k;
   const __nv_bfloat16* v;
   long long k_rs, k_hs, v_rs, v_hs;
@@ -55,8 +57,8 @@ struct Append {
   int32_t* flags;
   int total, hkv, num_slots;
   int window;      // rows whose runs one CTA handles, at most 16
-  int heads_per;   // kv heads of a CTA
-  int head_chunks; // CTAs that share a window's heads
+  int items_per;   // items of a CTA: the K heads, then the V heads
+  int chunks;      // CTAs that share a window's items
 };
 
 constexpr int PAIRS = WARPS / 2;       // pairs of warps, each with its own run
@@ -192,16 +194,17 @@ __device__ __forceinline__ void write_run(const uint4 (*stage)[THREADS],
 template <int D, bool FP8, bool INTER>
 __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  if ((int)blockIdx.x < a.q_blocks) {
-    const int group = blockIdx.x / a.rows.tiles;
-    rotary::turn_rows<__nv_bfloat16, __nv_bfloat16, INTER, D, true>(a.rows, a.turn, blockIdx.x - group * a.rows.tiles,
-                                                                    group, smem);
+  const int item = blockIdx.x;
+  if (item >= a.kv_blocks) {
+    const int q_item = item - a.kv_blocks, group = q_item / a.rows.tiles;
+    rotary::turn_rows<__nv_bfloat16, __nv_bfloat16, INTER, D, true>(a.rows, a.turn, q_item - group * a.rows.tiles, group,
+                                                                    smem);
     return;
   }
   AppendSmem& sm = *reinterpret_cast<AppendSmem*>(smem);
   const int lane = lane_id();
-  const int item = blockIdx.x - a.q_blocks, chunk = item % a.head_chunks;
-  const long long first = (long long)(item / a.head_chunks) * a.window;  // the window's first row
+  const int chunk = item % a.chunks;
+  const long long first = (long long)(item / a.chunks) * a.window;  // the window's first row
   // Lane i holds the slot of row first - 1 + i: the window's rows, the one in
   // front of it and the 15 that a run may reach into behind it.
   const long long row = first - 1 + lane;
@@ -214,8 +217,8 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
   const bool follows = lane >= 1 && good && (slot & (BS - 1)) != 0 && before == slot - 1;
   const unsigned runs = __ballot_sync(FULL, mine && good && !follows), rest = __ballot_sync(FULL, follows);
   if (runs == 0) return;
-  // The pair's runs: item by item (kv head, K or V), and in each the window's runs.
-  const int h0 = chunk * a.heads_per, items = 2 * (min(a.hkv, h0 + a.heads_per) - h0);
+  // The pair's runs: item by item (K or V of a head), and in each the window's runs.
+  const int it0 = chunk * a.items_per, items = min(2 * a.hkv - it0, a.items_per);
   const int rotary_dim = a.turn.rotary_dim;
   struct Cursor {
     int it;
@@ -234,17 +237,18 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
     if (c.it < items) {
       int i, n;
       run_of(c, i, n);
-      const int off0 = __shfl_sync(FULL, slot, i) % BS, h = h0 + (c.it >> 1);
-      const bool is_v = c.it & 1;
+      const int off0 = __shfl_sync(FULL, slot, i) % BS, which = it0 + c.it;
+      const bool is_v = which >= a.hkv;
+      const int h = is_v ? which - a.hkv : which;
       fetch_run<D>(is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs, is_v ? a.v_rs : a.k_rs, is_v ? 0 : rotary_dim,
-                          (int)(first - 1 + i), n, off0, sm.ring[stage]);
+                   (int)(first - 1 + i), n, off0, sm.ring[stage]);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   Cursor now = {warp_id() / 2, runs}, next = now;
   int stage = 0;
   fetch(next, 0);
-  const int pairs = rotary_dim / 2;
+  const int pairs = it0 < a.hkv ? rotary_dim / 2 : 0;
   if (pairs > 0) {
     // The rows of the runs: from a run's first row to the last that follows it.
     unsigned rows = runs;
@@ -261,8 +265,8 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     int i, n;
     run_of(now, i, n);
-    const bool is_v = now.it & 1;
-    const int h = h0 + (now.it >> 1), at = __shfl_sync(FULL, slot, i);
+    const bool is_v = it0 + now.it >= a.hkv;
+    const int h = it0 + now.it - (is_v ? a.hkv : 0), at = __shfl_sync(FULL, slot, i);
     const long long blk = (long long)(at / BS) * a.hkv + h;
     write_run<D, FP8, INTER>(sm.ring[stage], !is_v && pairs > 0 ? sm.turn + (i - 1) : nullptr, rotary_dim, n, at % BS,
                              (is_v ? a.v_cache : a.k_cache) + blk * (BS * D * (FP8 ? 1 : 2)),
@@ -368,7 +372,7 @@ static attn_status_t launch_append_kernel(const cache::Append& a, unsigned block
     return ATTN_OK;
   });
   if (st != ATTN_OK) return st;
-  kern<<<blocks, cache::THREADS, a.q_blocks ? SMEM : OWN, stream>>>(a);
+  kern<<<blocks, cache::THREADS, (int)blocks > a.kv_blocks ? SMEM : OWN, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -398,6 +402,7 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
   a.num_slots = p.num_blocks * cache::BS;
   const int sms = device_sm_count();
   const bool turn_q = p.q && p.num_q_heads > 0;
+  long long q_blocks = 0;
   // Queries that stay as and where they are need no pass.
   if (turn_q && !(p.rotary_dim == 0 && p.q == p.q_out && p.q_row_stride == p.qo_row_stride &&
                   p.q_head_stride == p.qo_head_stride)) {
@@ -410,28 +415,30 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
     r.q_hs = p.q_head_stride, r.q_rs = p.q_row_stride;
     r.qo_hs = p.qo_head_stride, r.qo_rs = p.qo_row_stride;
     rotary::plan_rows(r, p.head_dim, true, sms);
-    const long long q_blocks = (long long)r.tiles * r.head_groups;
+    q_blocks = (long long)r.tiles * r.head_groups;
     if (q_blocks > 0x3fffffffLL) return ATTN_ERR_INVALID_ARG;
-    a.q_blocks = (int)q_blocks;
   }
   // Rows per CTA: as few as keep the grid within two rounds, 16 at most. A decode
   // step has a run per row, and a CTA's runs follow one another; a chunk has one
   // run per 16 rows, and CTAs without one end at once. (512 rows of 8 heads, a
   // sequence each: 2 rows 15 us, 16 rows 30 us; a chunk of about 2000 rows: 8 rows
-  // 7 us, 1 row 11 us.) A window's heads are shared out to up to 16 CTAs per SM,
-  // down to two heads each (one run for each pair of warps): a window with a
-  // second run, at a sequence's start, then ends with the others, for angles that
-  // several CTAs compute (8504 rows of 8 heads: all heads 25 us, 4 heads 21 us, 2
-  // heads 20 us).
-  const int most = (p.num_kv_heads + 1) / 2;  // two heads: a head of K or V for each pair
+  // 7 us, 1 row 11 us.) A window's K heads and then its V heads are shared out to up
+  // to 16 CTAs per SM, down to four each (one run for each pair of warps): a window
+  // with a second run, at a sequence's start, then ends with the others, for angles
+  // that each CTA with K heads computes (8504 rows of 8 heads, keys and values: all
+  // heads 25 us, K and V of 4 heads 21 us, of 2 heads 20 us, four heads of K or of V
+  // 19 us).
+  const int most = (2 * p.num_kv_heads + cache::PAIRS - 1) / cache::PAIRS;
   a.window = 1;
   while (a.window < cache::BS && ((long long)p.total + a.window - 1) / a.window * most > 8LL * sms) a.window *= 2;
   const long long windows = ((long long)p.total + a.window - 1) / a.window;
   const long long chunks = 16LL * sms / windows;
-  a.heads_per = (int)(chunks >= most ? 2 : chunks > 1 ? (p.num_kv_heads + chunks - 1) / chunks : p.num_kv_heads);
-  a.head_chunks = (p.num_kv_heads + a.heads_per - 1) / a.heads_per;
-  const long long blocks = a.q_blocks + windows * a.head_chunks;
+  const int heads = 2 * p.num_kv_heads;
+  a.items_per = (int)(chunks >= most ? cache::PAIRS : chunks > 1 ? (heads + chunks - 1) / chunks : heads);
+  a.chunks = (heads + a.items_per - 1) / a.items_per;
+  const long long blocks = q_blocks + windows * a.chunks;
   if (blocks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
+  a.kv_blocks = (int)(blocks - q_blocks);
   const bool fp8 = p.kv_dtype == ATTN_DTYPE_FP8_E4M3, inter = p.interleaved != 0;
   if (p.head_dim == 128)
     return fp8 ? launch_append_d<128, true>(a, inter, (unsigned)blocks, stream)

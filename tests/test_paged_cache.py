@@ -288,6 +288,22 @@ def test_append_fp8_matches_definition(lib, D, interleaved, old, new):
 
 
 @gpu
+@pytest.mark.parametrize("new,Hk", [([1, 40, 16], 1), ([300, 33, 700], 5), ([2000, 1200, 1600], 20)])
+def test_append_shares_heads_out(lib, new, Hk):
+    """One CTA for all heads of K and V, CTAs of either, and CTAs that hold the last heads of K and the first of V."""
+    c = _append_case([5, 0, 31], new, Hk, Hk, 64, True, 16)
+    freq = ref.frequencies(64)
+    q, dev, flags = _run_append(lib, c, freq, 1.0, False)
+    assert flags == 0
+    turn = lambda x: ref.rotate_ref(x.double(), c["pos"][:, None], freq)  # noqa: E731
+    want, size = turn(c["q"])
+    _within(q, want, size * ref.TURN_REL + want.abs() * BF16 * 1.001, "q")
+    want, size = turn(c["k"])
+    _check_pages(c, dev, "k", want, size * ref.TURN_REL)
+    _check_pages(c, dev, "v", c["v"].double(), torch.zeros_like(c["v"], dtype=torch.float64))
+
+
+@gpu
 @pytest.mark.parametrize("D", [64, 128])
 def test_append_bf16_any_order(lib, D):
     c = _append_case([5, 0, 31], [40, 16, 1], 4, 2, D, False, 12)
