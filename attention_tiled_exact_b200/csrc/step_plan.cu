@@ -5,12 +5,13 @@
 // Every CTA scans the requests itself (a few integers per thread, from L2)
 // instead of waiting for another's sums, keeps a chunk of the prefix sums in
 // shared memory, and fills its share of the chunk's rows four at a time: one
-// binary search for the first row's request, then a walk. A step of up to
-// SMALL rows is one CTA, which also advances the state. A larger one takes as
+// binary search for the first row's request, then a walk (one at a time in a
+// small step: 4.1 us for 64 rows of 64 requests, 5.3 us four at a time). A step of
+// up to SMALL rows is one CTA, which also advances the state. A larger one takes as
 // many CTAs as its rows fill, and a dependent launch of one CTA advances the
 // state after all of them, because the new state may lie over the old one.
 // The bytes are few (8 per token out): what bounds it is the launch and the
-// chain load - scan - search - load. One token for each of 64 sequences: 5.6 us;
+// chain load - scan - search - load. One token for each of 64 sequences: 4.1 us;
 // 225,000 rows of 300 requests: 6.6 us (53 us by one cluster of 8 CTAs, a row at a time).
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -119,6 +120,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   if constexpr (!ADVANCE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int faults = 0;
   const int used = used_before(a, faults);
+  // A thread's rows: in a small step one, because rows of different requests
+  // follow one another, each with its load of a table or free-list entry.
+  const int rows = ADVANCE && a.total_q <= THREADS ? 1 : 4;
+  bool advanced = false;
   long long tok_before = 0, blk_before = 0;  // of the chunks so far
   for (int c0 = 0; c0 < a.batch; c0 += CHUNK) {
     const int count = min(CHUNK, a.batch - c0);
@@ -150,12 +155,21 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
     }
     tok_before += tok_all;
     blk_before += blk_all;
+    if (ADVANCE && a.batch <= CHUNK && tok_before <= a.total_q) {  // every row of every request has its place
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int j = threadIdx.x * PER + i;
+        if (j < count) a.seq_out[j] = s[i] + n[i];
+      }
+      if (threadIdx.x == 0) a.used_out[0] = (int)min(used + blk_before, (long long)a.num_free);
+      advanced = true;
+    }
     if (threadIdx.x == 0) s_cu[count] = (int)min(tok_before, (long long)a.total_q);
     __syncthreads();
     const int begin = s_cu[0], end = s_cu[count];
-    // Rows 4 i .. 4 i + 3, as far as they are the chunk's.
-    for (int i = begin / 4 + rank * THREADS + threadIdx.x; 4LL * i < end; i += ranks * THREADS) {
-      const int t0 = max(4 * i, begin), t1 = (int)min(4LL * i + 4, (long long)end);
+    // Rows 4 i .. 4 i + 3 (or row i), as far as they are the chunk's.
+    for (int i = begin / rows + rank * THREADS + threadIdx.x; (long long)rows * i < end; i += ranks * THREADS) {
+      const int t0 = max(rows * i, begin), t1 = (int)min((long long)rows * i + rows, (long long)end);
       int lo = 0, hi = count;  // the last request whose first row is <= t0: it has row t0
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
       int id = -1, known = -1;  // the block of column `known` of request lo
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = 4 * i + j;
+        const int t = rows * i + j;
         if (t < t0 || t >= t1) continue;
         while (t >= s_cu[lo + 1]) ++lo, known = -1;  // past requests without rows too
         const int p = s_seq[lo] + (t - s_cu[lo]);
@@ -195,7 +209,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
       } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int t = 4 * i + j;
+          const int t = rows * i + j;
           if (t >= t0 && t < t1) a.positions[t] = pos[j], a.slots[t] = slot[j];
         }
       }
@@ -210,7 +224,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   if (tok_before > a.total_q) faults |= ATTN_FAULT_BAD_LENGTH;
   if (faults && a.flags) atomicOr(a.flags, faults);
   if (rank == 0 && threadIdx.x == 0) a.cu[a.batch] = (int)min(tok_before, (long long)a.total_q);
-  if constexpr (ADVANCE) {
+  if (ADVANCE && !advanced) {
     __syncthreads();
     advance_state(a, used, s_sums);
   }
