@@ -18,15 +18,16 @@
 //   from the fp32 turned key, not from a bf16 copy of it.
 //
 // Both kernels read and write each element once. 8504 rows of 32/8 heads of 128:
-// append 40 us (191 MB; the queries alone 23 us at 6.0 TB/s, the keys and values
-// alone 19 us, where a run's load, reduction and store follow one another),
-// gather 14 us (93 MB, 6.6 TB/s). A decode step of 32 rows takes 4.3 us and 3.7 us:
+// append 36 us (191 MB; the queries alone 23 us at 6.0 TB/s, the keys and values
+// alone 20 us, where a run's load, reduction and store follow one another),
+// gather 14 us (93 MB, 6.6 TB/s). A decode step of 32 rows takes 4.0 us and 3.7 us:
 // the launch and two dependent loads (slot, then row or block).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "block_scaled.cuh"
@@ -81,41 +82,50 @@ struct Lanes {
   __device__ __forceinline__ Lanes() : u(lane_id() % UNITS), grp(lane_id() / UNITS + (warp_id() & 1) * (GROUPS / 2)) {}
 };
 
-// Starts the copies of the lane's rows of a run (as in write_run) to its slots of a stage.
-template <int D>
+// Starts the copies of the lane's part of a run (as in write_run) to its slots of
+// a stage: of new tokens the rows, of kept ones (8-bit pages) the codes.
+template <int D, bool FP8>
 __device__ __forceinline__ void fetch_run(const __nv_bfloat16* x, long long rs, int rotary_dim, int t, int n, int off0,
-                                          uint4 (*stage)[THREADS]) {
+                                          const uint8_t* page, uint4 (*stage)[THREADS]) {
   using L = Lanes<D>;
   const L l;
   const int2 off = rotary::unit_offsets<D>(l.u, rotary_dim);
 #pragma unroll
   for (int i = 0; i < L::PER; ++i) {
     const int o = l.grp + L::GROUPS * i;
-    if (o < off0 || o >= off0 + n) continue;
-    const __nv_bfloat16* src = x + (long long)(t + o - off0) * rs;
+    const uint32_t to = smem_addr(&stage[2 * i][threadIdx.x]);
+    if (o >= off0 && o < off0 + n) {
+      const __nv_bfloat16* src = x + (long long)(t + o - off0) * rs;
 #pragma unroll
-    for (int v = 0; v < 2; ++v)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(&stage[2 * i + v][threadIdx.x])),
-                   "l"(src + (v ? off.y : off.x))
-                   : "memory");
+      for (int v = 0; v < 2; ++v)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + v * (THREADS * 16)),
+                     "l"(src + (v ? off.y : off.x))
+                     : "memory");
+    } else if (FP8 && o < off0) {
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + v * (THREADS * 16)),
+                     "l"(page + o * D + (v ? off.y : off.x))
+                     : "memory");
+    }
   }
 }
 
 // One run of `n` tokens from row `t` on, to offsets off0 .. off0 + n - 1 of a
 // block whose codes (or bf16 elements) of this head start at `page`, by a pair
-// of warps. turn: the angles of the first row, or NULL. amax_at: alternates from
-// run to run.
+// of warps. turn: the angles of the first row, or NULL. old_byte: the block's
+// scale so far, or -1 when nothing in front of the run is kept. amax_at: alternates
+// from run to run.
 template <int D, bool FP8, bool INTER>
 __device__ __forceinline__ void write_run(const uint4 (*stage)[THREADS],
-                                          const float2 (*turn)[rotary::MAX_PAIRS], int rotary_dim, int n, int off0, uint8_t* page, uint8_t* scale,
-                                          float (*amax_at)[2]) {
+                                          const float2 (*turn)[rotary::MAX_PAIRS], int rotary_dim, int n, int off0,
+                                          uint8_t* page, uint8_t* scale, int old_byte, float (*amax_at)[2]) {
   using L = Lanes<D>;
   constexpr int GROUPS = L::GROUPS, PER = L::PER;
   const L l;
   const int lane = lane_id(), pair = warp_id() / 2, half = warp_id() & 1, u = l.u, grp = l.grp;
   const bool turned = turn && u * 16 < rotary_dim;
   const int2 off = rotary::unit_offsets<D>(u, turn ? rotary_dim : 0);
-  const int old_byte = FP8 && off0 > 0 ? *scale : -1;
   const float old_scale = old_byte >= 0 ? bscale::scale_of(old_byte) : 0.f;
   float val[PER][16];
   float amax = 0.f;
@@ -126,8 +136,8 @@ __device__ __forceinline__ void write_run(const uint4 (*stage)[THREADS],
       rotary::load8(reinterpret_cast<const __nv_bfloat16*>(&stage[2 * i][threadIdx.x]), &val[i][0]);
       rotary::load8(reinterpret_cast<const __nv_bfloat16*>(&stage[2 * i + 1][threadIdx.x]), &val[i][8]);
     } else if (FP8 && o < off0) {
-      bscale::load_codes8(page + o * D + off.x, &val[i][0]);
-      bscale::load_codes8(page + o * D + off.y, &val[i][8]);
+      bscale::load_codes8(reinterpret_cast<const uint8_t*>(&stage[2 * i][threadIdx.x]), &val[i][0]);
+      bscale::load_codes8(reinterpret_cast<const uint8_t*>(&stage[2 * i + 1][threadIdx.x]), &val[i][8]);
 #pragma unroll
       for (int j = 0; j < 16; ++j) val[i][j] *= old_scale;
     } else {
@@ -233,21 +243,26 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
     i = __ffs(c.left) - 1;
     n = i == 31 ? 1 : 1 + __ffs(~(rest >> (i + 1))) - 1;  // rows that follow row i, and it
   };
+  // Starts the run's copies; its block's scale byte if tokens of the block are kept, or -1.
   auto fetch = [&](const Cursor& c, int stage) {
+    int byte = -1;
     if (c.it < items) {
       int i, n;
       run_of(c, i, n);
-      const int off0 = __shfl_sync(FULL, slot, i) % BS, which = it0 + c.it;
+      const int at = __shfl_sync(FULL, slot, i), off0 = at % BS, which = it0 + c.it;
       const bool is_v = which >= a.hkv;
       const int h = is_v ? which - a.hkv : which;
-      fetch_run<D>(is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs, is_v ? a.v_rs : a.k_rs, is_v ? 0 : rotary_dim,
-                   (int)(first - 1 + i), n, off0, sm.ring[stage]);
+      const long long blk = (long long)(at / BS) * a.hkv + h;
+      fetch_run<D, FP8>(is_v ? a.v + h * a.v_hs : a.k + h * a.k_hs, is_v ? a.v_rs : a.k_rs, is_v ? 0 : rotary_dim,
+                        (int)(first - 1 + i), n, off0, (is_v ? a.v_cache : a.k_cache) + blk * (BS * D * (FP8 ? 1 : 2)),
+                        sm.ring[stage]);
+      if (FP8 && off0 > 0) byte = (is_v ? a.v_scales : a.k_scales)[blk];
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return byte;
   };
   Cursor now = {warp_id() / 2, runs}, next = now;
-  int stage = 0;
-  fetch(next, 0);
+  int stage = 0, byte_now = fetch(next, 0);
   const int pairs = it0 < a.hkv ? rotary_dim / 2 : 0;
   if (pairs > 0) {
     // The rows of the runs: from a run's first row to the last that follows it.
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
   }
   while (now.it < items) {
     advance(next);
-    fetch(next, stage ^ 1);
+    const int byte_next = fetch(next, stage ^ 1);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
     int i, n;
     run_of(now, i, n);
@@ -270,8 +285,8 @@ __global__ void __launch_bounds__(THREADS, 4) append_kernel(const Append a) {
     const long long blk = (long long)(at / BS) * a.hkv + h;
     write_run<D, FP8, INTER>(sm.ring[stage], !is_v && pairs > 0 ? sm.turn + (i - 1) : nullptr, rotary_dim, n, at % BS,
                              (is_v ? a.v_cache : a.k_cache) + blk * (BS * D * (FP8 ? 1 : 2)),
-                             FP8 ? (is_v ? a.v_scales : a.k_scales) + blk : nullptr, sm.amax[stage]);
-    now = next;
+                             FP8 ? (is_v ? a.v_scales : a.k_scales) + blk : nullptr, byte_now, sm.amax[stage]);
+    now = next, byte_now = byte_next;
     stage ^= 1;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -422,19 +437,20 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
   // step has a run per row, and a CTA's runs follow one another; a chunk has one
   // run per 16 rows, and CTAs without one end at once. (512 rows of 8 heads, a
   // sequence each: 2 rows 15 us, 16 rows 30 us; a chunk of about 2000 rows: 8 rows
-  // 7 us, 1 row 11 us.) A window's K heads and then its V heads are shared out to up
-  // to 16 CTAs per SM, down to four each (one run for each pair of warps): a window
-  // with a second run, at a sequence's start, then ends with the others, for angles
-  // that each CTA with K heads computes (8504 rows of 8 heads, keys and values: all
-  // heads 25 us, K and V of 4 heads 21 us, of 2 heads 20 us, four heads of K or of V
-  // 19 us).
+  // 7 us, 1 row 11 us.) A window's K heads and then its V heads are shared out, in
+  // multiples of four (a run for each pair of warps), as long as the grid stays
+  // within two rounds: more CTAs compute more angles (8504 rows of 32/8 heads: 4
+  // heads of K or V each 39 us, 8 heads 36 us; 11567 rows of 64: 4 heads 32 us, all
+  // 16 28 us), fewer leave SMs empty (1071 rows of 32/8 heads of 128: 4 heads 7.6 us,
+  // 8 heads 9.9 us).
   const int most = (2 * p.num_kv_heads + cache::PAIRS - 1) / cache::PAIRS;
   a.window = 1;
   while (a.window < cache::BS && ((long long)p.total + a.window - 1) / a.window * most > 8LL * sms) a.window *= 2;
   const long long windows = ((long long)p.total + a.window - 1) / a.window;
-  const long long chunks = 16LL * sms / windows;
+  const long long chunks = std::max(1LL, 8LL * sms / windows);
   const int heads = 2 * p.num_kv_heads;
-  a.items_per = (int)(chunks >= most ? cache::PAIRS : chunks > 1 ? (heads + chunks - 1) / chunks : heads);
+  const long long items = (heads + chunks - 1) / chunks;
+  a.items_per = (int)std::min<long long>(heads, (items + cache::PAIRS - 1) / cache::PAIRS * cache::PAIRS);
   a.chunks = (heads + a.items_per - 1) / a.items_per;
   const long long blocks = q_blocks + windows * a.chunks;
   if (blocks > 0x7fffffffLL) return ATTN_ERR_INVALID_ARG;
