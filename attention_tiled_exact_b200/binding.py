@@ -756,6 +756,14 @@ def _opt(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _flags(t):
+    if t is None:
+        return 0
+    if t.dtype is not _I32 or t.numel() == 0:
+        raise ValueError("int32 error word")
+    return t.data_ptr()
+
+
 def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, total_q: int, num_blocks: int,
                     seq_lens_out=None, cu_seqlens_q=None, positions=None, slot_map=None, num_used_out=None,
                     error_flags=None):
@@ -801,7 +809,7 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
             raise ValueError("contiguous int32 tensors")
     p = _pack_plan(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(),
                    num_used.data_ptr(), seq_lens_out.data_ptr(), cu_seqlens_q.data_ptr(), positions.data_ptr(),
-                   slot_map.data_ptr(), num_used_out.data_ptr(), _opt(error_flags), B, columns, int(num_blocks),
+                   slot_map.data_ptr(), num_used_out.data_ptr(), _flags(error_flags), B, columns, int(num_blocks),
                    num_free, total_q, 16)
     _call(LIB.attn_plan_paged_step, "attn_plan_paged_step", index, p)
     return seq_lens_out, cu_seqlens_q, positions, slot_map, num_used_out
@@ -943,7 +951,7 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
         _i32_vec(positions, T, "positions")
         pos_ptr, freq_ptr = positions.data_ptr(), inv_freq.data_ptr()
     p = _pack_append(q_ptr, qo_ptr, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks_ptr, vs_ptr,
-                     slot_map.data_ptr(), pos_ptr, freq_ptr, _opt(error_flags), T, Hq, Hkv, D, NB, 16, rotary_dim,
+                     slot_map.data_ptr(), pos_ptr, freq_ptr, _flags(error_flags), T, Hq, Hkv, D, NB, 16, rotary_dim,
                      1 if interleaved else 0, magnitude, code, qs[0], qs[1], qo[0], qo[1], ks[0], ks[1], vs[0], vs[1])
     _call(LIB.attn_append_paged, "attn_append_paged", index, p)
     return q_out
@@ -972,7 +980,7 @@ def gather_paged(k_cache, v_cache, block_table, seq_lens, width: int, k_scales=N
         if t.shape != shape or t.dtype is not _BF16 or not t.is_contiguous():
             raise ValueError("contiguous bf16 outputs [B, Hkv, width, D]")
     p = _pack_gather(k_cache.data_ptr(), v_cache.data_ptr(), ks_ptr, vs_ptr, block_table.data_ptr(),
-                     seq_lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _opt(error_flags), B, Hkv, D, width, NB,
+                     seq_lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), _flags(error_flags), B, Hkv, D, width, NB,
                      16, columns, code)
     _call(LIB.attn_gather_paged, "attn_gather_paged", index, p)
     return k_out, v_out
@@ -1011,7 +1019,7 @@ def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tab
         return out, lse
     p = _pack_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                      out.data_ptr(), _opt(lse), B, Hq, Hkv, D, 16, columns, NB, int(max_seq_len), int(num_splits),
-                     1.0 / math.sqrt(D) if scale is None else scale, _row_code(out.dtype), _opt(error_flags), code, 1.0,
+                     1.0 / math.sqrt(D) if scale is None else scale, _row_code(out.dtype), _flags(error_flags), code, 1.0,
                      1.0)
     _call_with_workspace(LIB.attn_decode_paged_block_scaled, "attn_decode_paged_block_scaled", index, p, ks_ptr,
                          vs_ptr, workspace, k_scales.device)
@@ -1068,7 +1076,7 @@ def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_ta
                       columns * 16 if max_seqlen_k is None else int(max_seqlen_k), *qv, 0, 0, 0, 0, 0, 0, *ov,
                       1.0 / math.sqrt(D) if scale is None else scale, 1 if causal else 0, _row_code(out.dtype),
                       _opt(seqlens_q), seqlens_k.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                      block_table.data_ptr(), columns, NB, 16, _opt(error_flags), _opt(cu_seqlens_q), total)
+                      block_table.data_ptr(), columns, NB, 16, _flags(error_flags), _opt(cu_seqlens_q), total)
     _call_with_workspace(LIB.attn_prefill_paged_block_scaled, "attn_prefill_paged_block_scaled", index, p, ks_ptr,
                          vs_ptr, workspace, k_scales.device)
     return out, lse

@@ -715,8 +715,9 @@ static attn_status_t launch(Args a, int num_splits, void* workspace, size_t* byt
   if (ctas == 1) return launch_grid<D, HALVES, false, 4>(a, ctas, stream);
   // A warp's blocks follow one another, 0.6 us each, so a grid that leaves SMs
   // empty deals a CTA's blocks to 8 warps: one sequence of 4097 tokens, 32/8 heads,
-  // 9.1 us (4 warps 10.3), of 32768 tokens, 8/1 heads, 11.3 us (12.5). Fuller
-  // grids measure alike with either (b = 8, 4096 tokens: 17 us).
+  // 9.1 us (4 warps 10.3), of 32768 tokens, 8/1 heads, 11.3 us (12.5). A
+  // grid of several CTAs per SM has the warps already, and with 8 it takes two
+  // rounds (8 sequences of 4096 tokens, 3.5 CTAs per SM: 4 warps 17 us, 8 22 us).
   const bool wide = (long long)ctas * a.batch * a.tiles * a.hkv <= WIDE_CTAS * (long long)sms;
   return wide ? launch_grid<D, HALVES, true, 8>(a, ctas, stream) : launch_grid<D, HALVES, true, 4>(a, ctas, stream);
 }

@@ -770,6 +770,23 @@ def test_decode_block_scaled_strided_views_are_refused(lib):
 
 
 @gpu
+def test_error_words_of_another_type_are_refused(lib):
+    c = _decode_case([40, 40], 4, 2, 64, 61)
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")]
+    lens, q = _i32(c["lens"]).cuda(), c["q"].cuda()
+    rows, slots = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda"), _i32([-1, -1]).cuda()
+    one = _i32([0]).cuda()
+    for flags in (torch.zeros(8, dtype=torch.uint8, device="cuda")[1:], torch.zeros(0, dtype=torch.int32, device="cuda")):
+        for call in (lambda: lib.decode_paged_block_scaled(q, *dev, lens, error_flags=flags),
+                     lambda: lib.prefill_paged_block_scaled(q[:, :, None], *dev, lens, error_flags=flags),
+                     lambda: lib.append_paged(rows, rows, slots, *dev[:4], error_flags=flags),
+                     lambda: lib.gather_paged(dev[0], dev[1], dev[4], lens, 40, dev[2], dev[3], error_flags=flags),
+                     lambda: lib.plan_paged_step(lens.clone(), slots, dev[4], slots, one, 0, 9, error_flags=flags)):
+            with pytest.raises(ValueError):
+                call()
+
+
+@gpu
 def test_debug_build_finds_nothing(lib):
     """The bounds-checking build over decode (one and several clusters) and both prefill paths: no flag."""
     code = """
