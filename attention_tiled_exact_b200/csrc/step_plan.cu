@@ -7,12 +7,13 @@
 // shared memory, and fills its share of the chunk's rows four at a time: one
 // binary search for the first row's request, then a walk (one at a time in a
 // small step: 4.1 us for 64 rows of 64 requests, 5.3 us four at a time). A step of
-// up to SMALL rows is one CTA, which also advances the state. A larger one takes as
-// many CTAs as its rows fill, and a dependent launch of one CTA advances the
-// state after all of them, because the new state may lie over the old one.
+// up to SMALL rows is one CTA, a larger one takes as many CTAs as its rows fill.
+// The first CTA also advances the state; if the new state lies over the old one,
+// which the others may still be reading, a dependent launch of one CTA does.
 // The bytes are few (8 per token out): what bounds it is the launch and the
 // chain load - scan - search - load. One token for each of 64 sequences: 4.1 us;
-// 225,000 rows of 300 requests: 6.6 us (53 us by one cluster of 8 CTAs, a row at a time).
+// 225,000 rows of 300 requests: 5.3 us (53 us by one cluster of 8 CTAs, a row at a
+// time), over the old state 6.6 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -110,6 +111,8 @@ __device__ __forceinline__ void advance_state(const Args& a, int used, long long
   if (threadIdx.x == 0) a.used_out[0] = (int)min(used + all, (long long)a.num_free);
 }
 
+// ADVANCE: the first CTA advances the state. More than one may run with it only if
+// the new state is apart from the old one.
 template <bool ADVANCE>
 __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   __shared__ int s_cu[CHUNK + 1];    // the chunk's first rows, clipped to total_q
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
     }
     tok_before += tok_all;
     blk_before += blk_all;
-    if (ADVANCE && a.batch <= CHUNK && tok_before <= a.total_q) {  // every row of every request has its place
+    if (ADVANCE && rank == 0 && a.batch <= CHUNK && tok_before <= a.total_q) {  // every row of every request has its place
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const int j = threadIdx.x * PER + i;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   if (tok_before > a.total_q) faults |= ATTN_FAULT_BAD_LENGTH;
   if (faults && a.flags) atomicOr(a.flags, faults);
   if (rank == 0 && threadIdx.x == 0) a.cu[a.batch] = (int)min(tok_before, (long long)a.total_q);
-  if (ADVANCE && !advanced) {
+  if (ADVANCE && rank == 0 && !advanced) {
     __syncthreads();
     advance_state(a, used, s_sums);
   }
@@ -244,12 +247,15 @@ attn_status_t launch_plan(const attn_plan_params& p, cudaStream_t stream) {
   const plan::Args a = {p.seq_lens, p.new_lens, p.block_table, p.free_blocks, p.num_used, p.seq_lens_out,
                         p.cu_seqlens_q, p.positions, p.slot_map, p.num_used_out, p.error_flags, p.batch,
                         p.max_blocks_per_seq, p.num_blocks, p.num_free, p.total_q, vec ? 1 : 0};
-  if (p.total_q <= plan::SMALL) {
-    plan::plan_kernel<true><<<1, plan::THREADS, 0, stream>>>(a);
+  const int want = p.total_q <= plan::SMALL ? 1 : (p.total_q + plan::SMALL - 1) / plan::SMALL, sms = device_sm_count();
+  const int ctas = want < sms ? want : sms;
+  const bool apart = (p.seq_lens_out + p.batch <= p.seq_lens || p.seq_lens + p.batch <= p.seq_lens_out) &&
+                     p.num_used_out != p.num_used;
+  if (ctas == 1 || apart) {
+    plan::plan_kernel<true><<<ctas, plan::THREADS, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   }
-  const int want = (p.total_q + plan::SMALL - 1) / plan::SMALL, sms = device_sm_count();
-  plan::plan_kernel<false><<<want < sms ? want : sms, plan::THREADS, 0, stream>>>(a);
+  plan::plan_kernel<false><<<ctas, plan::THREADS, 0, stream>>>(a);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -69,9 +69,11 @@ def test_plan_matches_token_by_token(lib, batch, most, context):
 
 
 @gpu
-@pytest.mark.parametrize("batch,most,every", [(70, 25, 1), (2300, 1, 1), (2300, 1, 7), (2300, 2, 9), (512, 1, 1)])
-def test_plan_of_one_block_in_place(lib, batch, most, every):
-    """Up to 2048 rows, up to 512 and above; more requests than one scan holds, most of them idle; over the old state."""
+@pytest.mark.parametrize("batch,most,every", [(70, 25, 1), (2300, 1, 1), (2300, 1, 7), (2300, 2, 9), (512, 1, 1), (300, 40, 1),
+                                              (2300, 5, 1)])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_plan_advances_the_state(lib, batch, most, every, in_place):
+    """Up to 512 rows, up to 2048 and above; more requests than one scan holds, most of them idle; over the old state."""
     seq, new, table, free, blocks = _plan_case(batch, 40 + batch, most, 33)
     new[torch.arange(batch) % every != 0] = 0
     total = int(new.sum()) + 2
@@ -80,7 +82,8 @@ def test_plan_of_one_block_in_place(lib, batch, most, every):
         want = ref.plan_ref(seq, fit, table, free, 1, total - clip, None)
         d = [t.cuda() for t in (seq, new, table, free, _i32([1]))]
         flags = torch.zeros(1, dtype=torch.int32, device="cuda")
-        out = lib.plan_paged_step(*d, total - clip, blocks, seq_lens_out=d[0], num_used_out=d[4], error_flags=flags)
+        over = dict(seq_lens_out=d[0], num_used_out=d[4]) if in_place else {}
+        out = lib.plan_paged_step(*d, total - clip, blocks, error_flags=flags, **over)
         for name, x, y in zip(("lens", "cu", "positions", "slots", "used"), out, want):
             assert torch.equal(x.cpu(), y), name
         assert torch.equal(d[2].cpu(), want[5]) and int(flags.item()) == (lib.ATTN_FAULT_BAD_LENGTH if clip else 0)
