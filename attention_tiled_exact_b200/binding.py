@@ -687,7 +687,9 @@ _I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 def _packer(params):
     """The bytes of a parameter struct from its fields in order (pointers as ints, 0 for NULL)."""
     codes = {_vp: "P", _i32: "i", _i64: "q", ctypes.c_float: "f"}
-    return struct.Struct("@" + "".join(codes[t] for _, t in params._fields_)).pack
+    fields = "@" + "".join(codes[t] for _, t in params._fields_)
+    # With the padding behind the last field: the C side may copy the whole struct.
+    return struct.Struct(f"{fields}{ctypes.sizeof(params) - struct.calcsize(fields)}x").pack
 
 
 _pack_plan, _pack_rotary, _pack_append = _packer(PlanParams), _packer(RotaryParams), _packer(AppendParams)
