@@ -776,8 +776,9 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     further blocks a sequence needs are taken from free_blocks (int32) at
     num_used (int32 [1]) and entered. total_q (host) is the number of rows of
     the packed step, at least the sum of new_lens; rows behind that sum get
-    position and slot -1, which :func:`rotary` and :func:`append_paged` skip.
-    num_blocks is the pool's size. seq_lens_out may be seq_lens and
+    position and slot -1, which :func:`rotary` and :func:`append_paged` skip;
+    so do the rows of tokens that a sequence's table row has no place for (the
+    other sequences keep their rows). num_blocks is the pool's size. seq_lens_out may be seq_lens and
     num_used_out num_used: the state then advances in place.
     Returns ``(seq_lens_out [B], cu_seqlens_q [B + 1], positions [total_q],
     slot_map [total_q], num_used_out [1])``.

@@ -69,19 +69,20 @@ __device__ __forceinline__ void scan_pair(long long& tok, long long& blk, long l
   __syncthreads();
 }
 
-// A request's lengths, bounded to its table row.
-__device__ __forceinline__ void lengths(const Args& a, int b, int& s, int& n, int& faults) {
+// A request's cached and new tokens, bounded to its table row, and the rows that
+// its new tokens have in the step: all that it asks for, because the caller's rows
+// lie by that, and a request over its limit must not move those behind it.
+__device__ __forceinline__ void lengths(const Args& a, int b, int& s, int& n, int& asked, int& faults) {
   const int cap = a.max_blocks * BS;
   s = a.seq_lens[b];
-  n = a.new_lens[b];
+  asked = a.new_lens[b];
   if (s < 0 || s > cap) {
     faults |= ATTN_FAULT_BAD_LENGTH;
     s = s < 0 ? 0 : cap;
   }
-  if (n < 0 || n > cap - s) {
-    faults |= ATTN_FAULT_BAD_LENGTH;
-    n = n < 0 ? 0 : cap - s;
-  }
+  if (asked < 0 || asked > cap - s) faults |= ATTN_FAULT_BAD_LENGTH;
+  asked = max(asked, 0);
+  n = min(asked, cap - s);
 }
 
 __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + BS - 1) / BS; }
@@ -100,9 +101,9 @@ __device__ __forceinline__ void advance_state(const Args& a, int used, long long
   long long none = 0, taken = 0;
   int ignored = 0;  // the fill has flagged them
   for (int b = threadIdx.x; b < a.batch; b += THREADS) {
-    int s, n;
-    lengths(a, b, s, n, ignored);
-    const int end = s + a.cu[b + 1] - a.cu[b];
+    int s, n, asked;
+    lengths(a, b, s, n, asked, ignored);
+    const int end = s + min(n, a.cu[b + 1] - a.cu[b]);
     taken += blocks_of(end) - blocks_of(s);
     a.seq_out[b] = end;
   }
@@ -126,18 +127,20 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   // A thread's rows: in a small step one, because rows of different requests
   // follow one another, each with its load of a table or free-list entry.
   const int rows = ADVANCE && a.total_q <= THREADS ? 1 : 4;
-  bool advanced = false;
-  long long tok_before = 0, blk_before = 0;  // of the chunks so far
+  const int cap = a.max_blocks * BS;
+  bool advanced = false, dropped = false;    // dropped: some request asks for more than its table row holds
+  long long tok_before = 0, blk_before = 0;  // rows and blocks of the chunks so far
+  int last = 0;  // the end of the rows that this thread's requests have a token for
   for (int c0 = 0; c0 < a.batch; c0 += CHUNK) {
     const int count = min(CHUNK, a.batch - c0);
-    int s[PER], n[PER];
+    int s[PER], n[PER], asked[PER];
     long long tok = 0, blk = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int j = threadIdx.x * PER + i;
-      s[i] = n[i] = 0;
-      if (j < count) lengths(a, c0 + j, s[i], n[i], faults);
-      tok += n[i];
+      s[i] = n[i] = asked[i] = 0;
+      if (j < count) lengths(a, c0 + j, s[i], n[i], asked[i], faults);
+      tok += asked[i];
       blk += blocks_of(s[i] + n[i]) - blocks_of(s[i]);
     }
     long long tok_all, blk_all;
@@ -152,8 +155,9 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
         s_seq[j] = s[i];
         s_base[j] = (int)min(blk, (long long)a.num_free);
         if (rank == 0) a.cu[c0 + j] = s_cu[j];
+        if (n[i] > 0 && tok < a.total_q) last = (int)min(tok + n[i], (long long)a.total_q);
       }
-      tok += n[i];
+      tok += asked[i];
       blk += blocks_of(s[i] + n[i]) - blocks_of(s[i]);
     }
     tok_before += tok_all;
@@ -185,7 +189,12 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
         const int t = rows * i + j;
         if (t < t0 || t >= t1) continue;
         while (t >= s_cu[lo + 1]) ++lo, known = -1;  // past requests without rows too
-        const int p = s_seq[lo] + (t - s_cu[lo]);
+        const int nth = t - s_cu[lo];
+        if (nth >= cap - s_seq[lo]) {  // a row without a token
+          pos[j] = slot[j] = -1;
+          continue;
+        }
+        const int p = s_seq[lo] + nth;
         const int col = p / BS, had = blocks_of(s_seq[lo]);
         if (col != known) {
           known = col;
@@ -217,7 +226,10 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
         }
       }
     }
-    __syncthreads();  // the chunk's sums are overwritten next
+    bool cut = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) cut |= n[i] < asked[i];
+    dropped |= __syncthreads_or(cut) != 0;  // and the chunk's sums are overwritten next
   }
   for (long long t = min(tok_before, (long long)a.total_q) + rank * THREADS + threadIdx.x; t < a.total_q;
        t += ranks * THREADS) {
@@ -226,8 +238,22 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
   }
   if (tok_before > a.total_q) faults |= ATTN_FAULT_BAD_LENGTH;
   if (faults && a.flags) atomicOr(a.flags, faults);
-  if (rank == 0 && threadIdx.x == 0) a.cu[a.batch] = (int)min(tok_before, (long long)a.total_q);
-  if (ADVANCE && rank == 0 && !advanced) {
+  if (rank != 0) return;
+  int end = (int)min(tok_before, (long long)a.total_q);
+  if (dropped) {
+    // The step ends behind its last token: rows without one belong to a request
+    // only where a later request's tokens follow.
+#pragma unroll
+    for (int d = 16; d; d >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
+    if (lane_id() == 0) s_sums[warp_id()][0] = last;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 32; ++w) last = max(last, (int)s_sums[w][0]);
+    end = last;
+    for (int b = threadIdx.x; b < a.batch; b += THREADS)
+      if (a.cu[b] > end) a.cu[b] = end;
+  }
+  if (threadIdx.x == 0) a.cu[a.batch] = end;
+  if (ADVANCE && !advanced) {
     __syncthreads();
     advance_state(a, used, s_sums);
   }

@@ -595,7 +595,8 @@ ATTN_API attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t st
  * free_blocks[num_used[0] ...]. Outputs:
  *   block_table  the new entries, from column ceil(seq_lens[b] / 16) on
  *   seq_lens_out [batch] seq_lens + new_lens
- *   cu_seqlens_q [batch + 1] prefix sums of new_lens (the packed rows)
+ *   cu_seqlens_q [batch + 1] prefix sums of new_lens (the packed rows), up to
+ *                the end of the last row that has a token
  *   positions    [total_q] each new token's position in its sequence
  *   slot_map     [total_q] its slot: block * 16 + position % 16
  *   num_used_out [1] num_used plus the blocks taken
@@ -604,12 +605,16 @@ ATTN_API attn_status_t attn_rotary(const attn_rotary_params* p, attn_stream_t st
  * more rows than it has. seq_lens_out may be seq_lens and num_used_out may be
  * num_used (the state advances in place, so a captured step can be replayed);
  * other outputs overlap nothing.
- * Faults (error_flags): ATTN_FAULT_BAD_LENGTH for a negative length, a
- * sequence over max_blocks_per_seq * 16 tokens or more than total_q new
- * tokens (the new tokens past either bound are dropped: no row, no block, and
- * seq_lens_out and num_used_out do not count them); ATTN_FAULT_NO_BLOCK when the free list runs out and
- * ATTN_FAULT_BAD_BLOCK for an id outside [0, num_blocks): the entry and its
- * tokens' slots are then -1.
+ * Faults (error_flags): ATTN_FAULT_BAD_LENGTH for a negative length (taken as
+ * 0), a sequence over max_blocks_per_seq * 16 tokens or more than total_q new
+ * tokens. The new tokens past either bound are dropped: they get no block, and
+ * seq_lens_out and num_used_out do not count them. A sequence over its limit
+ * keeps the rows that new_lens gives it, those of dropped tokens with position
+ * and slot -1, so that the rows of the sequences behind it stay where they are.
+ * (Attention calls take a sequence's rows as its last tokens: with dropped rows
+ * among them its own outputs of that step are not its tokens', the others' are.)
+ * ATTN_FAULT_NO_BLOCK when the free list runs out and ATTN_FAULT_BAD_BLOCK for
+ * an id outside [0, num_blocks): the entry and its tokens' slots are then -1.
  * Requirements: block_size == 16, num_blocks * 16 <= 2^31 - 1, batch <= 65535.
  */
 typedef struct {
