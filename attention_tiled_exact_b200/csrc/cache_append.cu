@@ -464,7 +464,9 @@ attn_status_t launch_append(const attn_append_params& p, cudaStream_t stream) {
 }
 
 attn_status_t launch_gather(const attn_gather_params& p, int zero_to, bool flag_width, cudaStream_t stream) {
-  const int blocks = (p.width + cache::BS - 1) / cache::BS;
+  // With flag_width even a width of 0 is launched: it flags the lengths, and the
+  // dependent launch behind it must not hang on whatever ran before.
+  const int blocks = std::max((p.width + cache::BS - 1) / cache::BS, flag_width ? 1 : 0);
   const long long items = (long long)p.batch * blocks * p.num_kv_heads;
   if (items == 0) return ATTN_OK;
   const long long grid = (items + cache::WARPS - 1) / cache::WARPS;

@@ -97,3 +97,23 @@ def test_a_full_sequence_leaves_the_others_alone(lib):
         assert torch.equal(vc[blk, :, off], rows[b, Hq + Hk:])
         kc[blk, :, off] = vc[blk, :, off] = 0
     assert not kc.any() and not vc.any()
+
+
+# ---------------------------------------------------------------------------- prefill over the 8-bit pages: paths that only some sizes take
+
+
+@gpu
+def test_prefill_block_scaled_of_no_keys_in_a_large_batch(lib):
+    """More row tiles than the few-rows kernel's grid has, and a bound of no keys: rows of 0, longer sequences flagged."""
+    B, D = 65600, 64
+    q = torch.randn(B, 1, D, generator=_gen(3)).to(torch.bfloat16).cuda()
+    pool, scales = torch.zeros(2, 1, 16, D, dtype=torch.uint8, device="cuda"), torch.full((2, 1), 127, dtype=torch.uint8, device="cuda")
+    table, lens = torch.zeros(B, 1, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for over in (0, 1):
+        lens[B - 3] = over
+        o, lse = lib.prefill_paged_block_scaled(q, pool, pool, scales, scales, table, lens, cu_seqlens_q=cu, max_seqlen_q=1,
+                                                max_seqlen_k=0, error_flags=flags)
+        assert (o == 0).all() and torch.isneginf(lse).all()
+        assert int(flags.item()) == (lib.ATTN_FAULT_BAD_LENGTH if over else 0)
