@@ -69,20 +69,16 @@ __device__ __forceinline__ void scan_pair(long long& tok, long long& blk, long l
   __syncthreads();
 }
 
-// A request's cached and new tokens, bounded to its table row, and the rows that
-// its new tokens have in the step: all that it asks for, because the caller's rows
-// lie by that, and a request over its limit must not move those behind it.
-__device__ __forceinline__ void lengths(const Args& a, int b, int& s, int& n, int& asked, int& faults) {
-  const int cap = a.max_blocks * BS;
-  s = a.seq_lens[b];
-  asked = a.new_lens[b];
-  if (s < 0 || s > cap) {
-    faults |= ATTN_FAULT_BAD_LENGTH;
-    s = s < 0 ? 0 : cap;
-  }
-  if (asked < 0 || asked > cap - s) faults |= ATTN_FAULT_BAD_LENGTH;
+// Bounds a request's cached tokens s and the new ones it asks for to its table row;
+// n: the new ones that it gets. Its rows in the step are all that it asks for,
+// because the caller's rows lie by that, and a request over its limit must not
+// move those behind it.
+__device__ __forceinline__ void bound(const Args& a, int& s, int& asked, int& n, int& faults) {
+  const int cap = a.max_blocks * BS, s0 = s, asked0 = asked;
+  s = min(max(s, 0), cap);
   asked = max(asked, 0);
   n = min(asked, cap - s);
+  if (s != s0 || n != asked0) faults |= ATTN_FAULT_BAD_LENGTH;
 }
 
 __device__ __forceinline__ int blocks_of(int tokens) { return (tokens + BS - 1) / BS; }
@@ -101,8 +97,8 @@ __device__ __forceinline__ void advance_state(const Args& a, int used, long long
   long long none = 0, taken = 0;
   int ignored = 0;  // the fill has flagged them
   for (int b = threadIdx.x; b < a.batch; b += THREADS) {
-    int s, n, asked;
-    lengths(a, b, s, n, asked, ignored);
+    int s = a.seq_lens[b], asked = a.new_lens[b], n;
+    bound(a, s, asked, n, ignored);
     const int end = s + min(n, a.cu[b + 1] - a.cu[b]);
     taken += blocks_of(end) - blocks_of(s);
     a.seq_out[b] = end;
@@ -138,8 +134,12 @@ __global__ void __launch_bounds__(THREADS) plan_kernel(const Args a) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int j = threadIdx.x * PER + i;
-      s[i] = n[i] = asked[i] = 0;
-      if (j < count) lengths(a, c0 + j, s[i], n[i], asked[i], faults);
+      s[i] = j < count ? a.seq_lens[c0 + j] : 0;
+      asked[i] = j < count ? a.new_lens[c0 + j] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      bound(a, s[i], asked[i], n[i], faults);
       tok += asked[i];
       blk += blocks_of(s[i] + n[i]) - blocks_of(s[i]);
     }
