@@ -9,7 +9,7 @@
 // in fp16, it keeps its own running maximum r of x_j + ev_j (in powers of two)
 // beside the softmax's running maximum m of x_j: the weight 2^(x_j + ev_j - r)
 // neither overflows nor vanishes while it matters, however far the exponents of
-// a sequence's blocks lie apart. Both maxima are kept stale until they grow by
+// a sequence's blocks lie apart (they reach over 2^230). Both maxima are kept stale until they grow by
 // 2^8.
 //
 // A tile is up to 8 * HALVES query rows of one sequence and kv head (row i: token
@@ -89,8 +89,8 @@ struct Args {
   void* o;
   float* lse;
   long long q_bs, q_hs, q_rs, o_bs, o_hs, o_rs, lse_bs, lse_hs;  // the LSE's row stride is 1
-  float* part_o;    // [cluster][tile of the grid][row][D], normalised
-  float* part_lse;  // [cluster][tile of the grid][row], natural log
+  float* part_o;     // [cluster][tile of the grid][row][D], normalised, in units of 2^shift
+  float2* part_lse;  // [cluster][tile of the grid][row]: LSE (natural log) and shift
   int o_f32, causal;
   int batch, max_q, total_q, hkv, group, max_blocks, num_blocks, max_len;
   int tiles;        // row tiles per sequence and kv head (a bound)
@@ -218,17 +218,30 @@ __device__ __forceinline__ void add_scaled(float4& acc, float w, const float4& x
   acc.x = fmaf(w, x.x, acc.x), acc.y = fmaf(w, x.y, acc.y), acc.z = fmaf(w, x.z, acc.z), acc.w = fmaf(w, x.w, acc.w);
 }
 
-// A row's sum and O (in units of 2^R, its sum in units of 2^M) as output and LSE.
-__device__ __forceinline__ float finish_row(float M, float R, float sum, float4& acc) {
+// Divides O (in units of 2^R) by a row's sum (in units of 2^M): O is then in units
+// of 2^shift. Returns the row's LSE.
+__device__ __forceinline__ float divide_row(float M, float R, float sum, float4& acc, float& shift) {
   const float Ms = M == -INFINITY ? 0.f : M, Rs = R == -INFINITY ? 0.f : R;
   const bool empty = sum == 0.f;  // a NaN is not an empty row
   const float inv = empty ? 0.f : 1.f / sum;
-  const float back = exp2f(0.5f * (Rs - Ms));  // applied twice: 2^(R - M) may leave fp32 where O does not
-  acc.x = empty ? 0.f : acc.x * inv * back * back;
-  acc.y = empty ? 0.f : acc.y * inv * back * back;
-  acc.z = empty ? 0.f : acc.z * inv * back * back;
-  acc.w = empty ? 0.f : acc.w * inv * back * back;
+  acc.x = empty ? 0.f : acc.x * inv;
+  acc.y = empty ? 0.f : acc.y * inv;
+  acc.z = empty ? 0.f : acc.z * inv;
+  acc.w = empty ? 0.f : acc.w * inv;
+  shift = empty ? 0.f : Rs - Ms;
   return empty ? -INFINITY : (Ms + log2f(sum)) * LN2;
+}
+
+// A row's sum and O as output and LSE.
+__device__ __forceinline__ float finish_row(float M, float R, float sum, float4& acc) {
+  float shift;
+  const float lse = divide_row(M, R, sum, acc, shift);
+  const float back = exp2f(0.5f * shift);  // applied twice: 2^shift may leave fp32 where O does not
+  acc.x = acc.x * back * back;
+  acc.y = acc.y * back * back;
+  acc.z = acc.z * back * back;
+  acc.w = acc.w * back * back;
+  return lse;
 }
 
 // CTAs of a cluster: the row of the grid up to CLUSTER.
@@ -439,15 +452,15 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_per_sm<D, HALVES>() * 4 / WAR
         float p[4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
+          // The softmax's weight for the sum, and the weight of the codes for O: an
+          // exponential of its own, because 2^(ev + m - r), its ratio to the other one,
+          // may be anything from 2^-250 to 2^250 (as fast as a product of the two: 8
+          // sequences of 4096 tokens 16.3 us).
           const float ms = m[h][j] == -INFINITY ? 0.f : m[h][j];
-          // 2^(ev + m - r): the softmax's weight to O's. Bounded, so that a weight of 0 stays 0.
-          float f = r[h][j] == -INFINITY ? ev : ev + ms - r[h][j];
-          f = ex2_approx(f > 126.f ? 126.f : f);
-          p[j] = ex2_approx(x[h][j] - ms);
-          p[2 + j] = ex2_approx(x[h][2 + j] - ms);
-          l[h][j] += p[j] + p[2 + j];
-          p[j] *= f;
-          p[2 + j] *= f;
+          const float up = r[h][j] == -INFINITY ? ev : ev - r[h][j];
+          l[h][j] += ex2_approx(x[h][j] - ms) + ex2_approx(x[h][2 + j] - ms);
+          p[j] = ex2_approx(x[h][j] + up);
+          p[2 + j] = ex2_approx(x[h][2 + j] + up);
         }
         // fp16 weights: half a step is 2^-11 of the weight, below the rounding of a bf16 result.
         pb[h][0] = transpose8x8(pack_f16x2(p[0], p[1]));
@@ -559,15 +572,17 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_per_sm<D, HALVES>() * 4 / WAR
         sum = fmaf(ex2_approx(m[c] - Ms), l[c], sum);
         add_scaled(acc, ex2_approx(r[c] - Rs), o[c]);
       }
-      const float lse = finish_row(M, R, sum, acc);
       if (!part) {
+        const float lse = finish_row(M, R, sum, acc);
         store_row4(a, grp, kvh, row, d, acc, lse);
       } else {
+        float shift;
+        const float lse = divide_row(M, R, sum, acc, shift);
         const long long at = (((long long)(split / CLUSTER) * gridDim.z + blockIdx.z) * a.hkv + kvh) * ROWS + row;
         if (ATTN_IN_BOUNDS(split / CLUSTER < (int)gridDim.x / CLUSTER && row < ROWS, ATTN_SITE_DECODE_PARTIAL,
                            a.error_flags, a.planted)) {
           *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
-          if (d == 0) a.part_lse[at] = lse;
+          if (d == 0) a.part_lse[at] = make_float2(lse, shift);
         }
       }
     }
@@ -576,12 +591,13 @@ __global__ void __launch_bounds__(32 * WARPS, ctas_per_sm<D, HALVES>() * 4 / WAR
 }
 
 // Merges the clusters' partial results of one row (blockIdx.x) of one tile and kv
-// head: O = sum_s e^(lse_s - lse) O_s, dealt out to 4 warps. A dependent launch:
-// it is set up while the last splits run.
+// head: O = sum_s e^(lse_s - lse) 2^(shift_s) O_s, dealt out to 4 warps. The weights
+// e^(lse_s) and e^(lse_s) 2^(shift_s) have their own maxima, as in the splits.
+// A dependent launch: it is set up while the last splits run.
 template <int D, int ROWS, int SPLIT_WARPS>
 __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const Args a, int ctas) {
   constexpr int PER = D / 32;
-  __shared__ float s_m[COMBINE_WARPS], s_sum[COMBINE_WARPS];
+  __shared__ float s_m[COMBINE_WARPS], s_r[COMBINE_WARPS], s_sum[COMBINE_WARPS];
   __shared__ __align__(16) float s_acc[COMBINE_WARPS][D];
   const int row = blockIdx.x, kvh = blockIdx.y, warp = warp_id(), lane = lane_id();
   const Group grp = group_of<ROWS, SPLIT_WARPS>(a, blockIdx.z, ctas);
@@ -589,22 +605,26 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const Args 
   if (row >= grp.rows || grp.used <= CLUSTER) return;
   const int n = (grp.used + CLUSTER - 1) / CLUSTER;
   const long long first = ((long long)blockIdx.z * a.hkv + kvh) * ROWS + row, step = (long long)gridDim.z * a.hkv * ROWS;
-  float M = -INFINITY;
-  for (int i = threadIdx.x; i < n; i += 32 * COMBINE_WARPS) M = fmaxf(M, __ldcg(a.part_lse + first + i * step));
+  float M = -INFINITY, R = -INFINITY;
+  for (int i = threadIdx.x; i < n; i += 32 * COMBINE_WARPS) {
+    const float2 y = __ldcg(a.part_lse + first + i * step);
+    M = fmaxf(M, y.x), R = fmaxf(R, fmaf(y.x, LOG2E, y.y));
+  }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, d));
-  if (lane == 0) s_m[warp] = M;
+  for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, d)), R = fmaxf(R, __shfl_xor_sync(FULL, R, d));
+  if (lane == 0) s_m[warp] = M, s_r[warp] = R;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < COMBINE_WARPS; ++w) M = fmaxf(M, s_m[w]);
-  const float Ms = M == -INFINITY ? 0.f : M;
+  for (int w = 0; w < COMBINE_WARPS; ++w) M = fmaxf(M, s_m[w]), R = fmaxf(R, s_r[w]);
+  const float Ms = M == -INFINITY ? 0.f : M, Rs = R == -INFINITY ? 0.f : R;
   float sum = 0.f, acc[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) acc[i] = 0.f;
 #pragma unroll 4
   for (int i = warp; i < n; i += COMBINE_WARPS) {
     if (!ATTN_IN_BOUNDS(i < ctas / CLUSTER, ATTN_SITE_COMBINE, a.error_flags, a.planted)) break;
-    const float w = ex2_approx((__ldcg(a.part_lse + first + i * step) - Ms) * LOG2E);
+    const float2 y = __ldcg(a.part_lse + first + i * step);
+    const float w = ex2_approx(fmaf(y.x, LOG2E, y.y) - Rs);
     const float* src = a.part_o + (first + i * step) * D + lane * PER;
     float x[PER];
     if constexpr (PER == 4) {
@@ -614,7 +634,7 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const Args 
       const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
       x[0] = v.x, x[1] = v.y;
     }
-    sum += w;
+    sum += ex2_approx((y.x - Ms) * LOG2E);
 #pragma unroll
     for (int k = 0; k < PER; ++k) acc[k] = fmaf(w, x[k], acc[k]);
   }
@@ -631,8 +651,8 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS) combine_kernel(const Args 
     sum += s_sum[w];
     add_scaled(out, 1.f, *reinterpret_cast<const float4*>(&s_acc[w][d]));
   }
-  // The weights are powers of e relative to Ms: in powers of two for finish_row.
-  const float lse = finish_row(Ms * LOG2E, Ms * LOG2E, sum, out);
+  // The sum is relative to a power of e: in powers of two for finish_row.
+  const float lse = finish_row(Ms * LOG2E, Rs, sum, out);
   store_row4(a, grp, kvh, row, d, out, lse);
 }
 
@@ -698,7 +718,7 @@ static attn_status_t launch_grid(const Args& a, int ctas, cudaStream_t stream) {
   return ATTN_ERR_CUDA;
 }
 
-// With `bytes` only the workspace's size: O, then LSE of the partial results.
+// With `bytes` only the workspace's size: O, then LSE and shift of the partial results.
 template <int D, int HALVES>
 static attn_status_t launch(Args a, int num_splits, void* workspace, size_t* bytes, cudaStream_t stream) {
   constexpr int ROWS = 8 * HALVES;
@@ -707,11 +727,11 @@ static attn_status_t launch(Args a, int num_splits, void* workspace, size_t* byt
   const size_t n = ctas > CLUSTER ? (size_t)(ctas / CLUSTER) * a.batch * a.tiles * a.hkv * ROWS : 0;
   const size_t lse_at = n * D * sizeof(float);
   if (bytes) {
-    *bytes = (lse_at + n * sizeof(float) + 255) / 256 * 256;
+    *bytes = (lse_at + n * sizeof(float2) + 255) / 256 * 256;
     return ATTN_OK;
   }
   a.part_o = reinterpret_cast<float*>(workspace);
-  a.part_lse = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + lse_at);
+  a.part_lse = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(workspace) + lse_at);
   if (ctas == 1) return launch_grid<D, HALVES, false, 4>(a, ctas, stream);
   // A warp's blocks follow one another, 0.6 us each, so a grid that leaves SMs
   // empty deals a CTA's blocks to 8 warps: one sequence of 4097 tokens, 32/8 heads,

@@ -721,7 +721,8 @@ ATTN_API attn_status_t attn_gather_paged(const attn_gather_params* p, attn_strea
  * its own length: into as many splits as the call finds best (num_splits == 0),
  * not at all (1), or into num_splits rounded down to a power of two up to 8 or
  * to a multiple of 8 (fewer where they would be shorter than 128 tokens).
- * Scales of the blocks of one sequence and head may differ by up to 2^100.
+ * Scales of the blocks of one sequence and head may lie as far apart as their
+ * bytes can say.
  */
 ATTN_API attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* p, const uint8_t* k_scales,
                                                       const uint8_t* v_scales, void* workspace,

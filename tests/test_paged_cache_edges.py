@@ -1,12 +1,13 @@
 """What the operators of a serving step over a paged cache do at their edges: requests over
 their limits, scales far apart, far positions, paths that only some sizes take, faults."""
 import ctypes
+import math
 
 import pytest
 import torch
 
 from tests import paged_cache_ref as ref
-from tests.test_paged_cache import _gen, _i32
+from tests.test_paged_cache import _attention_tol, _decode_case, _decode_run, _decode_want, _gen, _i32, _within
 
 gpu = pytest.mark.gpu
 STRUCTS = ("PlanParams", "RotaryParams", "AppendParams", "GatherParams", "DecodeParams", "PrefillParams")
@@ -117,3 +118,81 @@ def test_prefill_block_scaled_of_no_keys_in_a_large_batch(lib):
                                                 max_seqlen_k=0, error_flags=flags)
         assert (o == 0).all() and torch.isneginf(lse).all()
         assert int(flags.item()) == (lib.ATTN_FAULT_BAD_LENGTH if over else 0)
+
+
+# ---------------------------------------------------------------------------- value scales as far apart as their bytes allow
+
+# A weight's exponent is a sum of numbers below 2^8, each rounding of which is off by at most 2^-17: two in a
+# split, two in the merge of splits, one in the row's result: 5 * 2^-17 * ln 2 of the weight.
+FAR = 5 * 2.0 ** -17 * 0.6932
+
+
+def _balanced_case(lens, Hq, Hk, D, seed, order):
+    """Every block's scores lie around 2^t and its values around 2^-t, t in [-100, 100]: the blocks decide the output
+    alike, though their weights in the softmax are up to 2^200 apart. order: t ascends ("up"), descends, or is shuffled."""
+    g = _gen(seed)
+    c = _decode_case(lens, Hq, Hk, D, seed, 0.0)
+    c["q"] = (c["q"].float() * 0.1).to(torch.bfloat16)
+    c["q"][:, :, 0] = 1.0
+    c["scale"] = 1.0
+    for b, n in enumerate(lens):
+        blocks = (n + 15) // 16
+        t = torch.linspace(-100, 100, blocks) if blocks > 1 else torch.zeros(blocks)
+        t = {"up": t, "down": t.flip(0), "shuffled": t[torch.randperm(blocks, generator=g)]}[order]
+        k0 = (t * math.log(2)).to(torch.float8_e4m3fn)  # 4 significant bits: the values follow what it became
+        for j in range(blocks):
+            blk, live = int(c["table"][b, j]), min(16, n - 16 * j)
+            c["ks"][blk] = 127
+            c["kc"][blk, :, :live] = torch.randn(Hk, live, D, generator=g).to(torch.float8_e4m3fn).view(torch.uint8)
+            c["kc"][blk, :, :live, 0] = k0.view(torch.uint8)[j]
+            c["vs"][blk] = 120 - round(float(k0[j]) / math.log(2))
+    return c
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("order", ["up", "down", "shuffled"])
+def test_decode_block_scaled_scales_of_any_distance(lib, order, D):
+    c = _balanced_case([3000, 200, 33], 8, 2, D, 5 + D, order)
+    o, lse, tol, ltol = _decode_want(c)
+    pv = _values_sum(c)
+    for splits in (1, 0, 4, 16):
+        go, gl, flags = _decode_run(lib, c, num_splits=splits, out_dtype=torch.float32, max_seq_len=3000)
+        assert flags == 0
+        _within(go, o, tol + FAR * pv + 2.0 ** -21 * o.abs(), f"O splits {splits}")
+        _within(gl, lse, ltol, f"LSE splits {splits}")
+
+
+def _values_sum(c):
+    """sum_j p_j |v_j| of every row."""
+    kv, vv = ref.values(c["kc"], c["ks"]), ref.values(c["vc"], c["vs"])
+    out = []
+    for b, n in enumerate(c["lens"]):
+        ids = c["table"][b, : (n + 15) // 16].long()
+        k, v = (x[ids].transpose(0, 1).reshape(c["Hk"], -1, c["D"])[:, :n] for x in (kv, vv))
+        q = c["q"][b].double().reshape(c["Hk"], -1, c["D"])
+        out.append(ref.attend_ref(q, k, v, c["scale"], torch.full((q.shape[1],), n))[2].reshape(c["Hq"], c["D"]))
+    return torch.stack(out)
+
+
+@gpu
+@pytest.mark.parametrize("context", [500, 40000])
+@pytest.mark.parametrize("order", ["up", "shuffled"])
+def test_prefill_block_scaled_short_chunk_scales_of_any_distance(lib, order, context):
+    """Three rows go to the few-rows kernel: one cluster, and (40000 keys) several."""
+    rows, D, Hq, Hk = 3, 128, 4, 2
+    n = context + rows
+    c = _balanced_case([n], Hq, Hk, D, 7, order)
+    q = (torch.randn(1, Hq, rows, D, generator=_gen(9)) * 0.1).to(torch.bfloat16)
+    q[..., 0] = 1.0
+    dev = [c[k].cuda() for k in ("kc", "vc", "ks", "vs", "table")]
+    o, lse = lib.prefill_paged_block_scaled(q.cuda(), *dev, _i32([n]).cuda(), scale=1.0, out_dtype=torch.float32, max_seqlen_k=n)
+    ids = c["table"][0, : (n + 15) // 16].long()
+    k, v = (ref.values(c[a], c[s])[ids].transpose(0, 1).reshape(Hk, -1, D)[:, :n] for a, s in (("kc", "ks"), ("vc", "vs")))
+    ev = (c["vs"][ids].double() - 127).T.repeat_interleave(16, 1)[:, :n]
+    limit = torch.arange(context + 1, n + 1).repeat(Hq // Hk)
+    qs = q[0].double().reshape(Hk, Hq // Hk * rows, D)
+    want, wl, tol, ltol = _attention_tol(qs, k, ev, v, 1.0, limit, 2.0 ** -11, 2.0 ** -25)
+    pv = ref.attend_ref(qs, k, v, 1.0, limit)[2]
+    _within(o[0], want.reshape(Hq, rows, D), (tol + FAR * pv + 2.0 ** -21 * want.abs()).reshape(Hq, rows, D), "O")
+    _within(lse[0], wl.reshape(Hq, rows), ltol.reshape(Hq, rows), "LSE")
