@@ -42,15 +42,21 @@ __device__ __forceinline__ int unit_pair(int u, int i, int rotary_dim) {
 
 // magnitude * (cos, sin) of position * inv_freq[pair]. The angle is reduced to
 // half turns in fp64 (an fp32 product is off by half a step of the angle, 0.03
-// rad at position 10^6); the remainder, in [-1, 1], goes to fp32 as a sum hi + lo
+// rad at position 10^6), the product as a sum of two numbers: rounded to one it is
+// off by 2^-20.6 rad at 2^31 radians, with the second one by less than 2^-50 at
+// any position. The remainder, in [-1, 1], goes to fp32 as a sum hi + lo
 // whose second part enters to first order, cos(a + d) = cos a - d sin a: rounded
 // to hi alone it would be off by up to 2^-23.3 rad, more than all that follows,
 // and an 8-bit key is made from the result.
 __device__ __forceinline__ float2 pair_turn(const Turn& t, int position, int pair) {
-  constexpr double INV_PI = 0.31830988618379067154;
+  constexpr double INV_PI = 0.31830988618379067154, INV_PI_LO = -1.9678676675182486e-17;  // their sum is 1 / pi
   constexpr float PI = 3.14159265358979f;
-  double h = (double)position * (__ldg(t.inv_freq + pair) * INV_PI);
-  h -= 2.0 * rint(0.5 * h);
+  const double freq = __ldg(t.inv_freq + pair), at = (double)position;
+  const double f = freq * INV_PI, f_lo = fma(freq, INV_PI, -f) + freq * INV_PI_LO;
+  double h = at * f;
+  const double h_lo = fma(at, f, -h) + at * f_lo;
+  h -= 2.0 * rint(0.5 * h);  // exact
+  h += h_lo;
   const float hi = (float)h, d = PI * (float)(h - (double)hi);
   float si, co;
   sincospif(hi, &si, &co);

@@ -550,8 +550,8 @@ ATTN_API void attn_decode_graph_pool_destroy(attn_decode_graph_pool* pool);
  * on are copied. inv_freq (device, fp64, [rotary_dim / 2]) holds the angle of
  * each pair per position in radians, so every scaling for long contexts that
  * acts on the frequencies is a choice of inv_freq and m. The angle is reduced
- * in 64 bits and the turn is computed in fp32: positions up to 2^31 - 1 keep
- * the accuracy of near ones.
+ * in 64 bits, with the product's remainder, and the turn is computed in fp32:
+ * positions up to 2^31 - 1 keep the accuracy of near ones.
  * inverse != 0 turns by -a: the transpose of the map, which is its gradient
  * (attn_rotary of dQ / dK with inverse gives the gradients of the unrotated
  * q / k).

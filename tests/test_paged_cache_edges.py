@@ -2,6 +2,8 @@
 their limits, scales far apart, far positions, paths that only some sizes take, faults."""
 import ctypes
 import math
+from decimal import Decimal, getcontext
+from fractions import Fraction
 
 import pytest
 import torch
@@ -196,3 +198,31 @@ def test_prefill_block_scaled_short_chunk_scales_of_any_distance(lib, order, con
     pv = ref.attend_ref(qs, k, v, 1.0, limit)[2]
     _within(o[0], want.reshape(Hq, rows, D), (tol + FAR * pv + 2.0 ** -21 * want.abs()).reshape(Hq, rows, D), "O")
     _within(lse[0], wl.reshape(Hq, rows), ltol.reshape(Hq, rows), "LSE")
+
+
+# ---------------------------------------------------------------------------- rotary: far positions
+
+
+def _remainder(position, freq):
+    """position * freq (an fp64 number, exactly) modulo 2 pi, in [-pi, pi], rounded once to 64 bits."""
+    getcontext().prec = 60
+    tau = Fraction(2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494459"))
+    a = Fraction(freq) * position
+    return float(a - round(a / tau) * tau)
+
+
+@gpu
+@pytest.mark.parametrize("fast", [False, True])
+def test_rotary_keeps_its_accuracy_at_far_positions(lib, fast):
+    """fp32 rows at positions up to 2^31 - 1, both ways round, within the bound of near ones: the usual frequencies,
+    and up to a turn per position, where one 64-bit product would be off by 2^-18 rad."""
+    pos = [2 ** 31 - 1, 2 ** 31 - 1000, 2 ** 30 + 1, 2 ** 28 + 12345, 2 ** 27 - 7, 999999937, 5]
+    freq = torch.linspace(0.1, 6.2, 64, dtype=torch.float64) if fast else ref.frequencies(128)
+    x = torch.randn(len(pos), 3, 128, generator=_gen(3))
+    a = torch.tensor([[_remainder(p, f) for f in freq.tolist()] for p in pos], dtype=torch.float64)[:, None]
+    x1, x2 = x.double().split(64, -1)
+    size = torch.cat((x1.abs() + x2.abs(),) * 2, -1)
+    for sign, inverse in ((1.0, False), (-1.0, True)):
+        y, _ = lib.rotary(x.cuda(), None, freq.cuda(), _i32(pos).cuda(), inverse=inverse)
+        c, s = torch.cos(a), torch.sin(a) * sign
+        _within(y, torch.cat((x1 * c - x2 * s, x2 * c + x1 * s), -1), size * ref.TURN_REL, "far")
