@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(THREADS) gather_kernel(const Gather g, long lo
 
 template <int D, bool FP8, bool INTER>
 static attn_status_t launch_append_kernel(const cache::Append& a, unsigned blocks, cudaStream_t stream) {
-  // The query CTAs' ring, if there are any.
-  constexpr int RING = rotary::ring_bytes<__nv_bfloat16>(), OWN = (int)sizeof(cache::AppendSmem), SMEM = RING > OWN ? RING : OWN;
+  constexpr int SMEM = (int)sizeof(cache::AppendSmem);
+  static_assert(rotary::ring_bytes<__nv_bfloat16>() <= SMEM, "the query CTAs' ring");
   auto kern = cache::append_kernel<D, FP8, INTER>;
   static DeviceOnce setup;
   const attn_status_t st = setup.run([&]() -> attn_status_t {
@@ -387,7 +387,7 @@ static attn_status_t launch_append_kernel(const cache::Append& a, unsigned block
     return ATTN_OK;
   });
   if (st != ATTN_OK) return st;
-  kern<<<blocks, cache::THREADS, (int)blocks > a.kv_blocks ? SMEM : OWN, stream>>>(a);
+  kern<<<blocks, cache::THREADS, SMEM, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
