@@ -122,6 +122,124 @@ def test_prefill_block_scaled_of_no_keys_in_a_large_batch(lib):
         assert int(flags.item()) == (lib.ATTN_FAULT_BAD_LENGTH if over else 0)
 
 
+def _prefill_path(lib, B, Hq, Hk, D, rows, keys):
+    """Which kernel a chunk takes, from its workspace: "few" rows, or the tensor-core tiles with the keys of an item in
+    "whole" or dealt out in "shares"."""
+    p, need = lib.PrefillParams(), ctypes.c_size_t(0)
+    for name in ("q", "o", "seqlens_k", "k_cache", "v_cache", "block_table"):
+        setattr(p, name, 1 << 20)  # never read
+    p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim, p.seqlen_q, p.seqlen_k = B, Hq, Hk, D, rows, keys
+    p.scale, p.max_blocks_per_seq, p.num_blocks, p.block_size = 1.0, (keys + 15) // 16, 1 << 20, 16
+    p.q_row_stride = p.o_row_stride = D
+    assert lib.LIB.attn_prefill_paged_block_scaled(ctypes.byref(p), 1 << 20, 1 << 20, None, 0, ctypes.byref(need), None) == 0
+    dense = 2 * (-(-B * Hk * keys * D * 2 // 256) * 256)
+    return "few" if need.value < dense or not dense else "whole" if need.value == dense else "shares"
+
+
+def _check_chunks(c, q, cu, lens, o, lse, causal, what):
+    """Packed rows [T, Hq, D] and LSE [Hq, T] of a call over the case's pages against the definition."""
+    Hq, Hk, D = c["Hq"], c["Hk"], c["D"]
+    kv, vv = ref.values(c["kc"], c["ks"]), ref.values(c["vc"], c["vs"])
+    for b, n in enumerate(lens):
+        rows = cu[b + 1] - cu[b]
+        if rows == 0:
+            continue
+        ids = c["table"][b, : (n + 15) // 16].long()
+        k, v = (x[ids].transpose(0, 1).reshape(Hk, -1, D)[:, :n] for x in (kv, vv))
+        ev = (c["vs"][ids].double() - 127).T.repeat_interleave(16, 1)[:, :n]
+        limit = torch.arange(n - rows + 1, n + 1) if causal else torch.full((rows,), n)
+        qs = q[cu[b]:cu[b + 1]].double().permute(1, 0, 2).reshape(Hk, Hq // Hk * rows, D)
+        want, wl, tol, ltol = _attention_tol(qs, k, ev, v, c["scale"], limit.repeat(Hq // Hk), 2.0 ** -8 + 2.0 ** -11, 0)
+        want, tol, wl, ltol = (x.reshape(Hq, rows, *x.shape[2:]) for x in (want, tol, wl, ltol))
+        _within(o[cu[b]:cu[b + 1]].transpose(0, 1), want, tol + 2.0 ** -20 * want.abs(), f"{what} O {b}")
+        # the running sum is made of exponentials within 2^-12 of the exact ones
+        _within(lse[:, cu[b]:cu[b + 1]], wl, ltol + 2.0 ** -12, f"{what} LSE {b}")
+
+
+def _run_chunks(lib, c, q, chunks, lens, keys, causal, packed, flags=None):
+    """The call in packed or padded rows; O and LSE as packed ones, with the rows behind a padded sequence checked."""
+    cu = [0] + torch.cumsum(torch.tensor(chunks), 0).tolist()
+    most, Hq, D = max(chunks), c["Hq"], c["D"]
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")] + [_i32(lens).cuda()]
+    kw = dict(scale=c["scale"], causal=causal, out_dtype=torch.float32, max_seqlen_k=keys, error_flags=flags)
+    if packed:
+        return lib.prefill_paged_block_scaled(q.cuda(), *dev, cu_seqlens_q=_i32(cu).cuda(), max_seqlen_q=most, **kw)
+    pad = torch.zeros(len(chunks), Hq, most, D, dtype=torch.bfloat16)
+    for b, n in enumerate(chunks):
+        pad[b, :, :n] = q[cu[b]:cu[b + 1]].transpose(0, 1)
+    out = torch.full(pad.shape, 7.0, device="cuda")
+    lse = torch.full(pad.shape[:3], 7.0, device="cuda")
+    lib.prefill_paged_block_scaled(pad.cuda(), *dev, seqlens_q=_i32(chunks).cuda(), out=out, lse=lse, **kw)
+    for b, n in enumerate(chunks):
+        assert (out[b, :, n:] == 7.0).all() and (lse[b, :, n:] == 7.0).all()
+    return (torch.cat([out[b, :, :n].transpose(0, 1) for b, n in enumerate(chunks)]),
+            torch.cat([lse[b, :, :n] for b, n in enumerate(chunks)], 1))
+
+
+WHOLE = [(128, 5, 5), (128, 4, 2), (128, 3, 1), (128, 8, 2), (128, 16, 2), (64, 5, 5), (64, 4, 2), (64, 9, 3), (64, 8, 2), (64, 16, 2)]
+# a first chunk, a sequence without rows, rows that see no key, one row, a chunk over earlier tokens, a full bound
+CHUNKS, LENS = [500, 0, 300, 1, 130, 512], [500, 30, 200, 77, 333, 512]
+
+
+@pytest.mark.parametrize("D,Hq,Hk", WHOLE)
+def test_prefill_block_scaled_short_keys_take_whole_items(lib, D, Hq, Hk):
+    assert _prefill_path(lib, len(CHUNKS), Hq, Hk, D, max(CHUNKS), 512) == "whole"
+
+
+@gpu
+@pytest.mark.parametrize("D,Hq,Hk", WHOLE)
+@pytest.mark.parametrize("packed", [True, False])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_block_scaled_whole_items_match_definition(lib, D, Hq, Hk, packed, causal):
+    """A bound of at most 512 keys and many rows, as the first chunks of a batch of prompts have them."""
+    c = _decode_case(LENS, Hq, Hk, D, 61)
+    q = torch.randn(sum(CHUNKS), Hq, D, generator=_gen(62)).to(torch.bfloat16)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, lse = _run_chunks(lib, c, q, CHUNKS, LENS, 512, causal, packed, flags)
+    cu = [0] + torch.cumsum(torch.tensor(CHUNKS), 0).tolist()
+    _check_chunks(c, q, cu, LENS, o, lse, causal, "whole")
+    if causal:  # 300 rows over 200 keys
+        assert (o[cu[2]:cu[2] + 100] == 0).all() and torch.isneginf(lse[:, cu[2]:cu[2] + 100]).all()
+    assert int(flags.item()) == 0
+
+
+@gpu
+@pytest.mark.parametrize("Hq,Hk", [(9, 3), (32, 4)])
+def test_prefill_block_scaled_many_items_over_long_keys(lib, Hq, Hk):
+    """More than 4096 items: each stays whole although the bound of the keys is long."""
+    B, D, g = 700, 64, _gen(63)
+    lens = [1 + int(x) for x in torch.randint(0, 60, (B,), generator=g)]
+    chunks = [min(n, int(x)) for n, x in zip(lens, torch.randint(0, 6, (B,), generator=g))]
+    lens[3], chunks[3], lens[400], chunks[400], lens[B - 1], chunks[B - 1] = 900, 256, 1300, 9, 777, 130
+    most = max(chunks)
+    assert _prefill_path(lib, B, Hq, Hk, D, most, 1300) == "whole"
+    assert _prefill_path(lib, 40, Hq, Hk, D, most, 1300) == "shares"
+    c = _decode_case(lens, Hq, Hk, D, 64)
+    q = torch.randn(sum(chunks), Hq, D, generator=g).to(torch.bfloat16)
+    o, lse = _run_chunks(lib, c, q, chunks, lens, 1300, True, True)
+    _check_chunks(c, q, [0] + torch.cumsum(torch.tensor(chunks), 0).tolist(), lens, o, lse, True, "many")
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_block_scaled_whole_items_nan_in_a_visible_key(lib, D):
+    rows, n, Hq, Hk = 500, 510, 8, 2
+    assert _prefill_path(lib, 4, Hq, Hk, D, rows, 510) == "whole"
+    c = _decode_case([n] * 4, Hq, Hk, D, 65)
+    q = torch.randn(4 * rows, Hq, D, generator=_gen(66)).to(torch.bfloat16)
+    at = [10, 17, 300, 509]
+    for b, t in enumerate(at):
+        c["kc"][int(c["table"][b, t // 16]), 1, t % 16, 3 + b] = 0x7F
+    o, lse = _run_chunks(lib, c, q, [rows] * 4, [n] * 4, n, True, True)
+    for b, t in enumerate(at):
+        x, y = o[b * rows:(b + 1) * rows].cpu(), lse[:, b * rows:(b + 1) * rows].cpu()
+        sees = torch.arange(n - rows, n) >= t
+        assert torch.isfinite(x[:, :4]).all() and torch.isfinite(y[:4]).all()
+        for h in range(4, 8):
+            assert torch.equal(torch.isnan(x[:, h]).all(-1), sees) and torch.equal(torch.isnan(y[h]), sees)
+            assert torch.isfinite(x[~sees, h]).all()
+
+
 # ---------------------------------------------------------------------------- value scales as far apart as their bytes allow
 
 # A weight's exponent is a sum of numbers below 2^8, each rounding of which is off by at most 2^-17: two in a
@@ -177,6 +295,18 @@ def _values_sum(c):
     return torch.stack(out)
 
 
+def _few_rows_want(c, q, table, n, limit):
+    """One sequence's rows [Hq, rows, D] by the definition, with the tolerances of the few-rows kernel."""
+    Hk, (Hq, rows, D) = c["Hk"], q.shape
+    ids = table[: (n + 15) // 16].long()
+    k, v = (ref.values(c[a], c[s])[ids].transpose(0, 1).reshape(Hk, -1, D)[:, :n] for a, s in (("kc", "ks"), ("vc", "vs")))
+    ev = (c["vs"][ids].double() - 127).T.repeat_interleave(16, 1)[:, :n]
+    qs, limit = q.double().reshape(Hk, Hq // Hk * rows, D), limit.repeat(Hq // Hk)
+    want, wl, tol, ltol = _attention_tol(qs, k, ev, v, c["scale"], limit, 2.0 ** -11, 2.0 ** -25)
+    tol = tol + FAR * ref.attend_ref(qs, k, v, c["scale"], limit)[2] + 2.0 ** -21 * want.abs()
+    return [x.reshape(Hq, rows, *x.shape[2:]) for x in (want, wl, tol, ltol)]
+
+
 @gpu
 @pytest.mark.parametrize("context", [500, 40000])
 @pytest.mark.parametrize("order", ["up", "shuffled"])
@@ -189,15 +319,9 @@ def test_prefill_block_scaled_short_chunk_scales_of_any_distance(lib, order, con
     q[..., 0] = 1.0
     dev = [c[k].cuda() for k in ("kc", "vc", "ks", "vs", "table")]
     o, lse = lib.prefill_paged_block_scaled(q.cuda(), *dev, _i32([n]).cuda(), scale=1.0, out_dtype=torch.float32, max_seqlen_k=n)
-    ids = c["table"][0, : (n + 15) // 16].long()
-    k, v = (ref.values(c[a], c[s])[ids].transpose(0, 1).reshape(Hk, -1, D)[:, :n] for a, s in (("kc", "ks"), ("vc", "vs")))
-    ev = (c["vs"][ids].double() - 127).T.repeat_interleave(16, 1)[:, :n]
-    limit = torch.arange(context + 1, n + 1).repeat(Hq // Hk)
-    qs = q[0].double().reshape(Hk, Hq // Hk * rows, D)
-    want, wl, tol, ltol = _attention_tol(qs, k, ev, v, 1.0, limit, 2.0 ** -11, 2.0 ** -25)
-    pv = ref.attend_ref(qs, k, v, 1.0, limit)[2]
-    _within(o[0], want.reshape(Hq, rows, D), (tol + FAR * pv + 2.0 ** -21 * want.abs()).reshape(Hq, rows, D), "O")
-    _within(lse[0], wl.reshape(Hq, rows), ltol.reshape(Hq, rows), "LSE")
+    want, wl, tol, ltol = _few_rows_want(c, q[0], c["table"][0], n, torch.arange(context + 1, n + 1))
+    _within(o[0], want, tol, "O")
+    _within(lse[0], wl, ltol, "LSE")
 
 
 # ---------------------------------------------------------------------------- rotary: far positions
