@@ -350,3 +350,88 @@ def test_rotary_keeps_its_accuracy_at_far_positions(lib, fast):
         y, _ = lib.rotary(x.cuda(), None, freq.cuda(), _i32(pos).cuda(), inverse=inverse)
         c, s = torch.cos(a), torch.sin(a) * sign
         _within(y, torch.cat((x1 * c - x2 * s, x2 * c + x1 * s), -1), size * ref.TURN_REL, "far")
+
+
+# ---------------------------------------------------------------------------- faults: what is left out, what is kept
+
+
+def _guarded(shape, dtype):
+    """A contiguous output inside a larger buffer of 7s, and the check that its surroundings are still 7."""
+    buf = torch.full((shape[0] + 8, *shape[1:]), 7.0, dtype=dtype, device="cuda")
+    return buf[4:-4], lambda: bool((buf[:4] == 7.0).all() and (buf[-4:] == 7.0).all())
+
+
+def _decode_guarded(lib, c, **kw):
+    B = len(c["lens"])
+    out, out_kept = _guarded((B, c["Hq"], c["D"]), torch.float32)
+    lse, lse_kept = _guarded((B, c["Hq"]), torch.float32)
+    _, _, flags = _decode_run(lib, c, out=out, lse=lse, **kw)
+    assert out_kept() and lse_kept()
+    return out, lse, flags
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [0, 1, 2, 16])
+def test_decode_block_scaled_leaves_the_keys_of_bad_blocks_out(lib, D, splits):
+    """An entry outside the pool in the middle, and at the end of a long sequence: flagged, its keys are not seen."""
+    c = _decode_case([64, 64, 2500], 4, 1, D, 9)
+    fine = {k: v for k, v in c.items()}
+    fine["table"], fine["lens"] = c["table"].clone(), [64, 48, 2496]
+    fine["table"][1, 2] = c["table"][1, 3]  # three blocks are left
+    want, wl, tol, ltol = _decode_want(fine)
+    for bad in (10 ** 6, -1):
+        c["table"][1, 2] = c["table"][2, 156] = bad  # the second one holds the last four tokens
+        o, lse, flags = _decode_guarded(lib, c, num_splits=splits)
+        assert flags == lib.ATTN_FAULT_BAD_BLOCK
+        _within(o, want, tol + 2.0 ** -21 * want.abs(), "O")
+        _within(lse, wl, ltol, "LSE")
+
+
+@gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("splits", [0, 1, 16])
+def test_decode_block_scaled_cuts_sequences_at_the_bound(lib, D, splits):
+    c = _decode_case([64, 10, 700], 4, 1, D, 10)
+    for bound in (30, 16, 400):
+        cut = {**c, "lens": [min(n, bound) for n in c["lens"]]}
+        want, wl, tol, ltol = _decode_want(cut)
+        o, lse, flags = _decode_guarded(lib, c, num_splits=splits, max_seq_len=bound)
+        assert flags == lib.ATTN_FAULT_BAD_LENGTH
+        _within(o, want, tol + 2.0 ** -21 * want.abs(), "O")
+        _within(lse, wl, ltol, "LSE")
+
+
+@gpu
+@pytest.mark.parametrize("rows,keys,path", [(3, 400, "few"), (400, 500, "whole"), (400, 2000, "shares")])
+def test_prefill_block_scaled_of_bad_blocks(lib, rows, keys, path):
+    """An entry outside the pool is flagged. The few-rows kernel leaves its keys out, the tensor-core tiles read zeros."""
+    Hq, Hk, D, B = 16, 2, 128, 2
+    assert _prefill_path(lib, B, Hq, Hk, D, rows, keys) == path
+    c = _decode_case([keys, keys - 7], Hq, Hk, D, 11)
+    q = torch.randn(B, Hq, rows, D, generator=_gen(12)).to(torch.bfloat16).cuda()
+    kw = dict(scale=c["scale"], causal=False, out_dtype=torch.float32, max_seqlen_k=keys)
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs")]
+    table, lens = c["table"].clone(), _i32(c["lens"])
+    spare = next(i for i in range(c["kc"].shape[0]) if i not in set(c["table"].flatten().tolist()))
+    if path == "few":
+        table[0, 5:-1] = c["table"][0, 6:].clone()  # one block less
+        exact = _few_rows_want(c, q[0].cpu(), table[0], keys - 16, torch.full((rows,), keys - 16))
+        table = c["table"].clone()
+    else:
+        table[0, 5] = spare
+        for t in dev[:2]:
+            t[spare] = 0
+        for t in dev[2:]:
+            t[spare] = 127
+    want, wl = lib.prefill_paged_block_scaled(q, *dev, table.cuda(), lens.cuda(), **kw)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table, lens = c["table"].clone(), _i32(c["lens"])
+    table[0, 5] = 10 ** 7
+    o, lse = lib.prefill_paged_block_scaled(q, *dev, table.cuda(), lens.cuda(), error_flags=flags, **kw)
+    assert int(flags.item()) == lib.ATTN_FAULT_BAD_BLOCK and torch.equal(o[1], want[1]) and torch.equal(lse[1], wl[1])
+    if path == "few":
+        _within(o[0], exact[0], exact[2], "O")
+        _within(lse[0], exact[1], exact[3], "LSE")
+    else:
+        assert torch.equal(o[0], want[0]) and torch.equal(lse[0], wl[0])
