@@ -435,3 +435,81 @@ def test_prefill_block_scaled_of_bad_blocks(lib, rows, keys, path):
         _within(lse[0], exact[1], exact[3], "LSE")
     else:
         assert torch.equal(o[0], want[0]) and torch.equal(lse[0], wl[0])
+
+
+# ---------------------------------------------------------------------------- graphs and streams
+
+
+@gpu
+@pytest.mark.parametrize("in_place", [True, False])
+def test_a_large_plan_is_replayed(lib, in_place):
+    """Many CTAs, and over the old state a dependent launch that advances it: captured once, replayed."""
+    B, most, width = 300, 40, 16
+    g = _gen(71)
+    seq, new = _i32(torch.randint(0, 100, (B,), generator=g)), _i32(torch.randint(0, most + 1, (B,), generator=g))
+    pages = torch.randperm(3 * B * width, generator=g).to(torch.int32)
+    table, free = pages[: B * width].reshape(B, width).clone(), pages[B * width:].contiguous()
+    total, cap = int(new.sum()) + 3, width * 16
+    assert total > 2048
+    d = [t.cuda() for t in (seq, new, table, free, _i32([0]))]
+    outs = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (B, B + 1, total, total, 1)]
+    if in_place:
+        outs[0], outs[4] = d[0], d[4]
+
+    def step():
+        lib.plan_paged_step(*d, total, 3 * B * width, seq_lens_out=outs[0], cu_seqlens_q=outs[1], positions=outs[2],
+                            slot_map=outs[3], num_used_out=outs[4])
+    start = [t.clone() for t in (d[0], d[2], d[4])]
+    step()
+    for t, x in zip((d[0], d[2], d[4]), start):
+        t.copy_(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    state = (seq, table, 0)
+    for _ in range(3):
+        graph.replay()
+        want = _plan_by_rows(state[0], new, state[1], free, state[2], total, cap)
+        for name, a, b in zip(("lens", "cu", "positions", "slots", "used", "table"), outs + [d[2]], want):
+            assert torch.equal(a.cpu(), b), name
+        if in_place:
+            state = (want[0], want[5], int(want[4]))
+        else:
+            state = (state[0], want[5], 0)
+
+
+@gpu
+@pytest.mark.parametrize("splits", [2, 16])
+def test_decode_block_scaled_in_a_graph_and_on_two_streams(lib, splits):
+    """One cluster and several: captured and replayed on two streams beside eager calls, as the lengths grow."""
+    cases = []
+    for seed in (81, 82):
+        c = _decode_case([3000, 70, 1, 900], 8, 2, 128, seed)
+        dev = [c[n].cuda() for n in ("q", "kc", "vc", "ks", "vs", "table")]
+        lens = _i32(c["lens"]).cuda()
+        cases.append((lens, lambda dev=dev, lens=lens: lib.decode_paged_block_scaled(*dev, lens, num_splits=splits, max_seq_len=3000)))
+    for _, f in cases:
+        f()
+    torch.cuda.synchronize()
+    graphs = []
+    for _, f in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = f()
+        graphs.append((graph, out))
+    streams = [torch.cuda.Stream() for _ in cases]
+    for lengths in ([3000, 70, 1, 900], [16, 0, 1, 17], [2999, 69, 0, 899]):
+        for lens, _ in cases:
+            lens.copy_(_i32(lengths))
+        want = [f() for _, f in cases]
+        torch.cuda.synchronize()
+        both = []
+        for (graph, _), (_, f), s in zip(graphs, cases, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+                both.append(f())
+        torch.cuda.synchronize()
+        for w, (_, o), e in zip(want, graphs, both):
+            for i in (0, 1):
+                assert torch.equal(w[i], o[i]) and torch.equal(w[i], e[i])
