@@ -731,6 +731,8 @@ def _call_with_workspace(fn, where, index, p, ks, vs, workspace, device):
             _check(fn(p, ks, vs, None, 0, need, None), where)
             workspace = torch.empty(need.value, dtype=_U8, device=device)
     if workspace is not None:
+        if not workspace.is_contiguous():  # its size is counted below
+            raise ValueError("contiguous workspace")
         status = fn(p, ks, vs, workspace.data_ptr(), workspace.numel() * workspace.element_size(), None, stream)
     if status:
         raise AttnError(status, where)

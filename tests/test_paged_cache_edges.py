@@ -437,6 +437,18 @@ def test_prefill_block_scaled_of_bad_blocks(lib, rows, keys, path):
         assert torch.equal(o[0], want[0]) and torch.equal(lse[0], wl[0])
 
 
+@gpu
+def test_workspaces_that_repeat_memory_are_refused(lib):
+    """An expanded tensor counts more elements than it has memory."""
+    c = _decode_case([2500, 40], 4, 2, 64, 13)
+    dev = [c[n].cuda() for n in ("kc", "vc", "ks", "vs", "table")] + [_i32(c["lens"]).cuda()]
+    q, wide = c["q"].cuda(), torch.zeros(256, dtype=torch.uint8, device="cuda").expand(1 << 16, 256)
+    with pytest.raises(ValueError):
+        lib.decode_paged_block_scaled(q, *dev, num_splits=16, workspace=wide)
+    with pytest.raises(ValueError):
+        lib.prefill_paged_block_scaled(q[:, :, None].expand(2, 4, 500, 64).contiguous(), *dev, workspace=wide)
+
+
 # ---------------------------------------------------------------------------- graphs and streams
 
 
