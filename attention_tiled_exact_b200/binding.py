@@ -917,8 +917,9 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
     """Write new tokens into a paged cache, with rotary positions if inv_freq is given.
 
     k, v [T,Hkv,D] bf16 (any row and head strides); slot_map (int32 [T]: block
-    * 16 + offset, negative: no token). The caches [num_blocks,Hkv,16,D] are
-    bf16, or E4M3 codes (uint8 / float8_e4m3fn) with k_scales / v_scales uint8
+    * 16 + offset, none twice; negative: no token). The caches
+    [num_blocks,Hkv,16,D] are bf16 (read by :func:`prefill_paged`, and with D
+    128 and 1, 2, 4 or 8 query heads per kv head by :func:`decode_paged`), or E4M3 codes (uint8 / float8_e4m3fn) with k_scales / v_scales uint8
     [num_blocks,Hkv], exponent bytes of a power-of-two scale for each block and
     head: the scale follows the block's tokens, and a run of new tokens replaces
     its block from its first slot on (consecutive rows, one run per block and
@@ -998,8 +999,9 @@ def decode_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tab
     """:func:`decode_paged` over the block-scaled 8-bit cache of :func:`append_paged`.
 
     q [B,Hq,D] bf16, D 64 or 128, up to 16 query heads per kv head; the caches
-    E4M3 codes with uint8 scales [num_blocks,Hkv]. Returns ``(O [B,Hq,D], LSE
-    [B,Hq] or None)``.
+    E4M3 codes with uint8 scales [num_blocks,Hkv]. Weights enter the product
+    with V in fp16, so float32 outputs are exact to about 2^-11 of sum p |v|.
+    Returns ``(O [B,Hq,D], LSE [B,Hq] or None)``.
     """
     index = _device_index(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, out, lse, workspace,
                           error_flags)
@@ -1038,7 +1040,9 @@ def prefill_paged_block_scaled(q, k_cache, v_cache, k_scales, v_scales, block_ta
     """:func:`prefill_paged` over the block-scaled 8-bit cache of :func:`append_paged`.
 
     max_seqlen_k (host int) bounds seqlens_k (None: the table's capacity); the
-    workspace grows with it. Returns ``(O, LSE)``.
+    workspace grows with it. Weights enter the product with V in fp16, or in
+    larger chunks in bf16, so float32 outputs are exact to about 2^-8 of
+    sum p |v|. Returns ``(O, LSE)``.
     """
     index = _device_index(q, k_cache, v_cache, k_scales, v_scales, block_table, seqlens_k, seqlens_q, out, lse,
                           workspace, error_flags, cu_seqlens_q)

@@ -18,9 +18,10 @@
 //   from the fp32 turned key, not from a bf16 copy of it.
 //
 // Both kernels read and write each element once. 8504 rows of 32/8 heads of 128:
-// append 36 us (191 MB; the queries alone 23 us at 6.0 TB/s, the keys and values
+// append 36 us (192 MB; the queries alone 23 us at 6.0 TB/s, the keys and values
 // alone 20 us, where a run's load, reduction and store follow one another),
-// gather 14 us (93 MB, 6.6 TB/s). A decode step of 32 rows takes 4.0 us and 3.7 us:
+// gather 14.5 us (93 MB, 6.4 TB/s); with bf16 pages 36 us (209 MB) and 21 us (119 MB,
+// 5.7 TB/s). A decode step of 32 rows takes 3.7 us and 3.5 us (bf16 3.0 and 3.7):
 // the launch and two dependent loads (slot, then row or block).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

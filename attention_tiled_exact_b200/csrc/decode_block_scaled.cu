@@ -39,9 +39,9 @@
 // round to fp16's step there, 2^-39 of the largest).
 //
 // Bound by HBM for full batches (64 sequences of 1K to 32K tokens, 32/8 heads of
-// 128: 324-335 us, 6.5-6.7 TB/s; the other order of the products, with a maximum
+// 128: 325-353 us, 6.2-6.7 TB/s; the other order of the products, with a maximum
 // per block, took 384 us) and by its chain of length, table, pages, products and
-// merge for few: one sequence of 4097 tokens 9.1 us, 8 of 4096 17 us (66 MB). The
+// merge for few: one sequence of 4097 tokens 9.2 us, 8 of 4096 16-17 us (66 MB). The
 // CTAs of a cluster read one another's results: sending them to the CTA that
 // merges them, ahead of one barrier instead of two, took 0.7 us longer.
 #include <cooperative_groups.h>
@@ -809,11 +809,16 @@ bool prefill_has_few_rows(const attn_prefill_params& p) {
   using namespace bsdecode;
   const long long tiles = ((long long)p.seqlen_q * (p.num_q_heads / p.num_kv_heads) + 15) / 16;
   if (p.batch * tiles > 65535 || p.num_kv_heads > 65535) return false;
-  // Estimates of both sides in ns, from the bounds of the lengths, fitted to
-  // measurements (chunk, context, query / kv heads, head_dim; this side against
-  // the other): 1, 6000, 8/1, 128: 10 against 28 us; 3 x 22, 3000, 16/4, 128: 16
-  // against 28; 4 x 16, 6000, 32/8, 128: 47 against 67; 4 x 100, 500, 32/8, 128: 37
-  // against 28; 5 x 300, 3000, 16/4, 128: 152 against 53.
+  // Estimates of both sides in ns, from the bounds of the lengths: which is the
+  // smaller is all that they are for, a call itself may take less than half or
+  // more than twice of one (few sequences fill no machine, ragged ones are shorter
+  // than their bound). Measured (chunk, context, query / kv heads, head_dim; this
+  // side against the other, in us): 1, 6000, 8/1, 128: 9.5 against 27; 3 x 22, 3000,
+  // 16/4, 128: 15.5 against 23; 4 x 16, 6000, 32/8, 128: 46 against 50; 4 x 100, 500,
+  // 32/8, 128: 26.5 against 27; 1 x 64, 30000, 32/8, 128: 146 against 82; 6 x 64, 3000,
+  // 32/8, 64: 56 against 35; 5 x 300, 3000, 16/4, 128: 138 against 49. Of 30 shapes it
+  // chooses the slower side of two, 4 x 100, 400, 8/2, 128 (18 against 14) and the
+  // fourth above.
   const int cap = p.max_blocks_per_seq * BS, len = p.seqlen_k < cap ? p.seqlen_k : cap;
   const double blocks = (len + BS - 1) / BS, wide = p.head_dim / 128.0;
   const double few = 4000 + p.batch * tiles * (double)p.num_kv_heads * blocks * (p.head_dim == 128 ? 1.1 : 0.45);

@@ -1,10 +1,10 @@
 // Rotary positions on dense or packed query / key rows (attn_rotary), for sm_100a.
 //
 // One pass: every row is read and written once (turn_rows). It is bound by HBM
-// for many rows: queries and keys of 4 x 40 heads x 2048 x 128 in bf16 take 28.4 us
-// (168 MB, 5.9 TB/s, of 6.4 TB/s of a plain elementwise kernel; the angles, with
-// which every CTA begins, cost 0.3 us of it), 8504 packed rows of 32 heads 23 us
-// (6.0 TB/s). 64 rows take 2.5 us, a launch and three dependent loads.
+// for many rows: queries and keys of 4 x 40 heads x 2048 x 128 in bf16 take 28.6-29.6
+// us (168 MB, 5.7-5.9 TB/s, of 6.4 TB/s of a plain elementwise kernel; the angles,
+// with which every CTA begins, cost 0.5 us of it), 8504 packed rows of 32 heads 21-23
+// us (6.1-6.6 TB/s). 64 rows take 2.5 us, a launch and three dependent loads.
 #include <cuda_runtime.h>
 #include <stdint.h>
 #include <string.h>

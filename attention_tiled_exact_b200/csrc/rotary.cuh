@@ -287,9 +287,9 @@ __device__ __forceinline__ void turn_rows(const Rows& r, const Turn& t, int tile
 // a tenth of a step per step for the chain of one CTA's loads, which few CTAs
 // hide. Over 100 shapes of 64 to 16384 rows, 8 to 64 query heads and both layouts
 // this is 0.8 % behind the best number on average. Queries and keys of 8192 tokens
-// and 40 heads of 128, by tokens: 4 groups 28.4 us, 1 group 29.9 us, 2 groups (one
-// round) 30.2 us, 40 groups 66 us; of 16384 tokens and 72 heads: 2 groups 98 us,
-// 1 group 111 us.
+// and 40 heads of 128, by tokens: 4 groups 27.9 us, 1 group 29.2 us, 2 groups (one
+// round) 29.2 us, 40 groups 69 us; of 16384 tokens and 72 heads: 2 groups 95 us,
+// 1 group 110 us.
 inline void plan_rows(Rows& r, int head_dim, bool by_heads, int sm_count) {
   const int rows = 32 / (head_dim / 16), warp_heads = by_heads ? rows : 1;
   r.by_heads = by_heads ? 1 : 0;

@@ -6,14 +6,14 @@
 // instead of waiting for another's sums, keeps a chunk of the prefix sums in
 // shared memory, and fills its share of the chunk's rows four at a time: one
 // binary search for the first row's request, then a walk (one at a time in a
-// small step: 4.1 us for 64 rows of 64 requests, 5.3 us four at a time). A step of
+// small step: 64 rows of 64 requests are 1.2 us faster than four at a time). A step of
 // up to SMALL rows is one CTA, a larger one takes as many CTAs as its rows fill.
 // The first CTA also advances the state; if the new state lies over the old one,
 // which the others may still be reading, a dependent launch of one CTA does.
 // The bytes are few (8 per token out): what bounds it is the launch and the
-// chain load - scan - search - load. One token for each of 64 sequences: 4.1 us;
-// 225,000 rows of 300 requests: 5.3 us (53 us by one cluster of 8 CTAs, a row at a
-// time), over the old state 6.6 us.
+// chain load - scan - search - load. One token for each of 64 sequences: 4.2 us;
+// 208,000 rows of 300 requests: 5.4 us (53 us by one cluster of 8 CTAs, a row at a
+// time), over the old state 6.8 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

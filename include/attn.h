@@ -650,7 +650,10 @@ ATTN_API attn_status_t attn_plan_paged_step(const attn_plan_params* p, attn_stre
  * without a token: nothing of it is written (its q row neither). With
  * rotary_dim == 0 nothing is rotated (positions and inv_freq are ignored);
  * q == NULL leaves the queries out.
- * kv_dtype BF16: the pages hold bf16 elements; slots may come in any order.
+ * kv_dtype BF16: the pages hold bf16 elements; slots may come in any order, but
+ * none twice. attn_prefill reads such pages for any head_dim and group of heads;
+ * attn_decode_paged only for head_dim 128 and 1, 2, 4 or 8 query heads per kv
+ * head.
  * kv_dtype FP8_E4M3: the new tokens of a block must be consecutive rows with
  * ascending consecutive slots (a step's rows are, see attn_plan_paged_step),
  * and a block may be written by one such run per call. The run replaces the
@@ -722,7 +725,17 @@ ATTN_API attn_status_t attn_gather_paged(const attn_gather_params* p, attn_strea
  * not at all (1), or into num_splits rounded down to a power of two up to 8 or
  * to a multiple of 8 (fewer where they would be shorter than 128 tokens).
  * Scales of the blocks of one sequence and head may lie as far apart as their
- * bytes can say.
+ * bytes can say. A block outside the pool is flagged (ATTN_FAULT_BAD_BLOCK) and
+ * its keys are left out.
+ * Precision: sums and statistics are fp32, and o_dtype F32 returns O without a
+ * further rounding, but the operands of the products are not fp32. The weight of
+ * a value (probability times scale) is rounded to fp16: by 2^-11 of itself, and
+ * by 2^-25 of the row's largest weight where it is below 2^-14 of that, while
+ * the sum that divides O is of unrounded ones. O is therefore off by about 2^-11
+ * of sum_j p_j |v_j| (a bf16 result's own rounding is 2^-8 of it), more where many
+ * keys have such small weights. Queries enter as fp16 scaled by the
+ * row's largest element: exact down to 2^-28 of it. The LSE has the rounding of
+ * fp32 sums of head_dim products.
  */
 ATTN_API attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* p, const uint8_t* k_scales,
                                                       const uint8_t* v_scales, void* workspace,
@@ -736,7 +749,13 @@ ATTN_API attn_status_t attn_decode_paged_block_scaled(const attn_decode_params* 
  * there and flagged (ATTN_FAULT_BAD_LENGTH). Workspace protocol as
  * attn_decode_paged; the size depends on the device's SM count. A NaN key makes
  * the rows that see it NaN; a NaN value may do so to other rows of its chunk
- * (their weight of 0 meets it in a tile's product).
+ * (their weight of 0 meets it in a tile's product). A block outside the pool is
+ * flagged (ATTN_FAULT_BAD_BLOCK); its keys are left out or, in larger chunks,
+ * read as zeros.
+ * Precision: chunks of few rows as the decode; larger ones go through the tiles
+ * of attn_prefill, where probabilities are rounded to bf16 (2^-8 of each) and a
+ * quarter of them comes from a polynomial: O is off by up to 2^-8 of sum_j p_j
+ * |v_j|, LSE by up to 2^-12, with o_dtype F32 too.
  */
 ATTN_API attn_status_t attn_prefill_paged_block_scaled(const attn_prefill_params* p, const uint8_t* k_scales,
                                                        const uint8_t* v_scales, void* workspace,
