@@ -780,8 +780,9 @@ def plan_paged_step(seq_lens, new_lens, block_table, free_blocks, num_used, tota
     the packed step, at least the sum of new_lens; rows behind that sum get
     position and slot -1, which :func:`rotary` and :func:`append_paged` skip;
     so do the rows of tokens that a sequence's table row has no place for (the
-    other sequences keep their rows). num_blocks is the pool's size. seq_lens_out may be seq_lens and
-    num_used_out num_used: the state then advances in place.
+    other sequences keep their rows). num_blocks is the pool's size.
+    seq_lens_out may be seq_lens and num_used_out num_used: the state then
+    advances in place.
     Returns ``(seq_lens_out [B], cu_seqlens_q [B + 1], positions [total_q],
     slot_map [total_q], num_used_out [1])``.
     """
@@ -919,7 +920,8 @@ def append_paged(k, v, slot_map, k_cache, v_cache, k_scales=None, v_scales=None,
     k, v [T,Hkv,D] bf16 (any row and head strides); slot_map (int32 [T]: block
     * 16 + offset, none twice; negative: no token). The caches
     [num_blocks,Hkv,16,D] are bf16 (read by :func:`prefill_paged`, and with D
-    128 and 1, 2, 4 or 8 query heads per kv head by :func:`decode_paged`), or E4M3 codes (uint8 / float8_e4m3fn) with k_scales / v_scales uint8
+    128 and 1, 2, 4 or 8 query heads per kv head by :func:`decode_paged`), or
+    E4M3 codes (uint8 / float8_e4m3fn) with k_scales / v_scales uint8
     [num_blocks,Hkv], exponent bytes of a power-of-two scale for each block and
     head: the scale follows the block's tokens, and a run of new tokens replaces
     its block from its first slot on (consecutive rows, one run per block and

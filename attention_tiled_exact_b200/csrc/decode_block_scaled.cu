@@ -9,8 +9,8 @@
 // in fp16, it keeps its own running maximum r of x_j + ev_j (in powers of two)
 // beside the softmax's running maximum m of x_j: the weight 2^(x_j + ev_j - r)
 // neither overflows nor vanishes while it matters, however far the exponents of
-// a sequence's blocks lie apart (they reach over 2^230). Both maxima are kept stale until they grow by
-// 2^8.
+// a sequence's blocks lie apart (they reach over 2^230). Both maxima are kept stale
+// until they grow by 2^8.
 //
 // A tile is up to 8 * HALVES query rows of one sequence and kv head (row i: token
 // i / group, head i % group); a block is read from HBM once for the tile. The
