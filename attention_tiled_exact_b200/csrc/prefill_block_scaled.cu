@@ -4,9 +4,10 @@
 // workspace as dense bf16 (code * 2^e has 4 significant bits, so that is exact) and
 // the dense prefill kernel attends to them. The first step moves 3 bytes per cached
 // element and kv head (and the second one 2 more), at HBM's rate; the second one is
-// bound by the softmax and tensor chain. 1844 rows over 30617 keys, 32/8 heads of 128: 30 us and 790-830 us
-// (1080-1140 TFLOP/s); 5 chunks of up to 300 rows over up to 3300 keys, 16/4 heads: 49
-// us in all; 8 first chunks of up to 512 rows, 32/8 heads: 46 us.
+// bound by the softmax and tensor chain. 1844 rows over 30617 keys, 32/8 heads of
+// 128: 30 us and 790-830 us (1080-1140 TFLOP/s); 5 chunks of up to 300 rows over up
+// to 3300 keys, 16/4 heads: 49 us in all; 8 first chunks of up to 512 rows, 32/8
+// heads: 46 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
